@@ -246,6 +246,162 @@ int mea_decode_paged(const void* q, const void* k_cache, const void* v_cache,
                      float scale, int mask_kind, const float* alibi_slopes, int dtype,
                      void* workspace, size_t workspace_bytes, int split_keys, void* stream);
 
+/*
+ * Operators on the paged K/V cache of mea_decode_paged, for long contexts and drafted tokens. All
+ * of them share its layout: k_cache, v_cache DEVICE [num_blocks, block_size, n_heads_kv, D] in
+ * MEA_F16 or MEA_BF16, block_size 16, 32 or a multiple of 64, block_table DEVICE int32
+ * [n_seqs, max_blocks], cu_seqlens_k DEVICE int32 [n_seqs + 1] prefix sums of the requests' key
+ * counts L_b, max_seqlen_k an upper bound on every L_b with max_blocks * block_size >=
+ * max_seqlen_k, D a multiple of 8 from 8 to 256. A block id outside [0, num_blocks) names no keys
+ * (reads give zeros, writes are left out). Slots past a request's end may hold any bits. No
+ * atomics on results: every result is deterministic. None of the calls allocates device memory or
+ * synchronises the host, and all can be captured into a CUDA graph; two calls that may run at
+ * the same time (two streams, two graphs) need a workspace each.
+ */
+
+/* Blocks per request that mea_select_blocks can choose from. */
+#define MEA_SELECT_MAX_BLOCKS 50000
+
+/*
+ * mea_block_key_bounds — the range of the keys in each cache block, per KV head and column:
+ *   bounds  DEVICE [num_blocks, n_heads_kv, 2, D], dtype of the cache; [blk][g][0] the least and
+ *           [blk][g][1] the greatest K[slot, g, :] of the block's existing slots (NaN if one is).
+ *   first_key  NULL: all blocks of every request. DEVICE int32 [n_seqs]: only request b's blocks
+ *              that hold a key >= first_key[b] (after a decode step: L_b - 1, one block).
+ * Blocks in no request's table keep their bounds. n_seqs <= 65535. A block that two requests share
+ * must be as full for both (a shared prefix of whole blocks is).
+ */
+int mea_block_key_bounds(const void* k_cache, const int32_t* block_table,
+                         const int32_t* cu_seqlens_k, const int32_t* first_key, void* bounds,
+                         int n_seqs, int num_blocks, int block_size, int max_blocks,
+                         int max_seqlen_k, int n_heads_kv, int head_dim, int dtype, void* stream);
+
+/*
+ * mea_select_blocks — the cache blocks a decode step attends to, per (request, KV head): the
+ * request's first n_first and last n_last blocks, then those with the greatest score
+ *   sum_d up[d] * bounds[blk][g][1][d] + down[d] * bounds[blk][g][0][d],
+ *   up = sum over the group's heads of max(q_h, 0), down = the same of min(q_h, 0),
+ * which bounds sum_h q_h . k from above for every key k of the block. The score is summed in 64
+ * bits and rounded to fp32 once; equal scores go to the lower block index (also where the first
+ * and last blocks alone exceed n_select), a NaN score ranks above every number.
+ *   q         DEVICE [n_seqs, n_heads_q, D], dtype of bounds.
+ *   selected  DEVICE int32 [n_seqs, n_heads_kv, n_select]: block indices within the request (places
+ *             in its block_table row), ascending, -1 after the last one when there are fewer.
+ * ceil(max_seqlen_k / block_size) <= MEA_SELECT_MAX_BLOCKS; a request's blocks past that many are
+ * not considered.
+ */
+int mea_select_blocks(const void* q, const void* bounds, const int32_t* block_table,
+                      const int32_t* cu_seqlens_k, int32_t* selected, int n_seqs, int num_blocks,
+                      int block_size, int max_blocks, int max_seqlen_k, int n_heads_q,
+                      int n_heads_kv, int head_dim, int n_select, int n_first, int n_last,
+                      int dtype, void* stream);
+
+/*
+ * mea_decode_selected — mea_decode_paged over the blocks that `selected` names for each (request,
+ * KV head) only: out and lse are those of a softmax over the keys of these blocks (positions for
+ * ALiBi are the keys' own). Entries are block indices within the request, in any order; an entry
+ * below 0 or past the request's blocks names no keys, and a block listed twice counts twice. A
+ * list that names no key gives out = 0, lse = -inf.
+ *   workspace  at least mea_decode_selected_workspace_size(...) bytes, 256-byte aligned.
+ *   split_keys listed keys per split-KV chunk, a multiple of 64 (rounded up to whole blocks); 0 =
+ *              the library's choice, as for mea_decode_splitkv.
+ */
+size_t mea_decode_selected_workspace_size(int n_seqs, int n_select, int block_size, int n_heads_q,
+                                          int n_heads_kv, int head_dim, int split_keys);
+int mea_decode_selected(const void* q, const void* k_cache, const void* v_cache,
+                        const int32_t* block_table, const int32_t* cu_seqlens_k,
+                        const int32_t* selected, void* out, float* lse, int n_seqs, int num_blocks,
+                        int block_size, int max_blocks, int n_select, int n_heads_q,
+                        int n_heads_kv, int head_dim, float scale, const float* alibi_slopes,
+                        int dtype, void* workspace, size_t workspace_bytes, int split_keys,
+                        void* stream);
+
+/*
+ * mea_decode_weights — mea_decode_paged that also gives each key's attention weight, summed over
+ * the query heads of its KV group and added to an earlier sum:
+ *   weights[b, g, t] = prev_weights[b, g, t] + sum over h in group g of exp(score_ht - lse_h)
+ * for 0 <= t < L_b; entries from L_b on are left as they were.
+ *   weights, prev_weights  DEVICE fp32 [n_seqs, n_heads_kv, weights_stride], weights_stride >=
+ *                          max_seqlen_k; prev_weights may be NULL (zeros) or weights itself.
+ *   workspace  at least mea_decode_weights_workspace_size(...) bytes, 256-byte aligned (the decode's
+ *              partials and one fp32 score per key and query head).
+ * total_k and split_keys as for mea_decode_paged; n_seqs <= 65535, n_heads_kv <= 65535.
+ */
+size_t mea_decode_weights_workspace_size(int n_seqs, int total_k, int n_heads_q, int n_heads_kv,
+                                         int head_dim, int split_keys);
+int mea_decode_weights(const void* q, const void* k_cache, const void* v_cache,
+                       const int32_t* block_table, const int32_t* cu_seqlens_k, void* out,
+                       float* lse, float* weights, const float* prev_weights,
+                       long long weights_stride, int n_seqs, int num_blocks, int block_size,
+                       int max_blocks, int total_k, int max_seqlen_k, int n_heads_q,
+                       int n_heads_kv, int head_dim, float scale, const float* alibi_slopes,
+                       int dtype, void* workspace, size_t workspace_bytes, int split_keys,
+                       void* stream);
+
+/*
+ * mea_attention_weights — the attention weight that the queries of a packed batch put on its keys:
+ *   weights[s, g, j] = sum over h in group g, over queries i of segment s, of exp(score_hij - lse_hi)
+ * for 0 <= j < L_k of the segment; entries from L_k on are left as they were. Segments, masks,
+ * GQA grouping, ALiBi, scale and the layouts of q and k as for mea_forward (D a multiple of 8 from 8 to
+ * 256); lse DEVICE fp32 [n_heads_q, total_q], the forward's.
+ *   weights       DEVICE fp32 [n_seqs, n_heads_kv, weights_stride], weights_stride >= max_seqlen_k.
+ *   last_queries  0: all queries; n > 0: each segment's last n only.
+ */
+int mea_attention_weights(const void* q, const void* k, const float* lse,
+                          const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                          float* weights, long long weights_stride, int n_seqs, int total_q,
+                          int total_k, int max_seqlen_q, int max_seqlen_k, int n_heads_q,
+                          int n_heads_kv, int head_dim, float scale, int mask_kind,
+                          const float* alibi_slopes, int last_queries, int dtype, void* stream);
+
+/*
+ * mea_evict_paged — keeps n_keep keys of each (request, KV head): its last n_recent, and of the
+ * others those with the greatest weight (equal weights: the lower index; a NaN ranks above every
+ * number). A request with L_b <= n_keep keeps all. The kept keys' K and V rows are copied, in
+ * their order, to slots 0, 1, ... of the request's new blocks.
+ *   weights      DEVICE fp32 [n_seqs, n_heads_kv, weights_stride], weights_stride >= max_seqlen_k.
+ *   out_table    DEVICE int32 [n_seqs, max_out_blocks], max_out_blocks * block_size >=
+ *                min(n_keep, max_seqlen_k): the new blocks, in the caches out_k_cache, out_v_cache
+ *                DEVICE [num_out_blocks, block_size, n_heads_kv, D]. These may be k_cache and v_cache
+ *                themselves, as long as no new block is one that a request still reads from.
+ *                Slots past the kept keys are left as they were.
+ *   kept         DEVICE int32 [n_seqs, n_heads_kv, n_keep]: the kept keys' indices, ascending, then -1.
+ *   out_weights  DEVICE fp32 [n_seqs, n_heads_kv, n_keep]: the kept keys' weights, then 0. Not weights.
+ *   out_cu_seqlens_k  DEVICE int32 [n_seqs + 1]: prefix sums of min(L_b, n_keep).
+ * Different heads keep different keys: afterwards slot t of a request holds another token's key for
+ * each head, so a position-dependent bias (ALiBi) no longer applies to the new cache.
+ */
+int mea_evict_paged(const void* k_cache, const void* v_cache, const int32_t* block_table,
+                    const int32_t* cu_seqlens_k, const float* weights, long long weights_stride,
+                    void* out_k_cache, void* out_v_cache, const int32_t* out_table, int32_t* kept,
+                    float* out_weights, int32_t* out_cu_seqlens_k, int n_seqs, int num_blocks,
+                    int num_out_blocks, int block_size, int max_blocks, int max_out_blocks,
+                    int max_seqlen_k, int n_heads_kv, int head_dim, int n_keep, int n_recent,
+                    int dtype, void* stream);
+
+/*
+ * mea_decode_tree — attention of drafted tokens over a paged cache (verification of a drafted tree).
+ * Request b has n_b = cu_seqlens_q[b+1] - cu_seqlens_q[b] drafted tokens, whose keys and values are
+ * the last n_b of its L_b cached ones; ctx = L_b - n_b. Drafted token i attends to every key t < ctx
+ * and to drafted token j (key ctx + j) when bit j of its mask row is set (its own bit included: a
+ * row without it does not see itself). A token that sees no key gets out = 0, lse = -inf.
+ *   q          DEVICE [total_q, n_heads_q, D], out the same, lse fp32 [n_heads_q, total_q] or NULL.
+ *   tree_mask  DEVICE int32 [total_q, mask_words], mask_words * 32 >= max_seqlen_q; bit j of a row is
+ *              bit j % 32 of word j / 32.
+ *   ALiBi      bias -slope[h] * |p_i - p_key|, with p = t for a context key and p = ctx + depth for
+ *              drafted token j, its depth the number of other tokens in its mask row.
+ *   workspace  at least mea_decode_tree_workspace_size(...) bytes, 256-byte aligned.
+ * Values of keys that only some of a request's tokens see must be finite, as in mea_forward.
+ */
+size_t mea_decode_tree_workspace_size(int n_heads_q, int n_heads_kv, int head_dim);
+int mea_decode_tree(const void* q, const void* k_cache, const void* v_cache,
+                    const int32_t* block_table, const int32_t* cu_seqlens_q,
+                    const int32_t* cu_seqlens_k, const int32_t* tree_mask, void* out, float* lse,
+                    int n_seqs, int total_q, int max_seqlen_q, int max_seqlen_k, int mask_words,
+                    int num_blocks, int block_size, int max_blocks, int n_heads_q,
+                    int n_heads_kv, int head_dim, float scale, const float* alibi_slopes,
+                    int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
 /* mea_status_string — a static English description of a mea_status value. */
 const char* mea_status_string(int status);
 

@@ -15,6 +15,11 @@ Public API (names follow the pages' vocabulary):
   gradients.
 * :func:`decode_splitkv` — one query token per request against a packed KV cache;
   :func:`decode_paged` against a block cache; :func:`decode_splitkv_noalloc` without a workspace.
+* On a block cache: :func:`decode_tree_paged` verifies a tree of drafted tokens
+  (:func:`tree_mask`); :func:`block_key_bounds`, :func:`select_blocks` and
+  :func:`decode_paged_selected` attend to the blocks that a cheap score picks;
+  :func:`attention_packed_weights` and :func:`decode_paged_weights` add up each key's attention
+  weight, and :func:`evict_paged` keeps the keys with the most of it.
 * :func:`alibi_slopes` — ``2^(-8(h+1)/H)``.
 
 Caller-provided outputs and workspaces must be contiguous tensors of exactly the documented
@@ -34,7 +39,11 @@ from ._lib import MeaError  # noqa: F401
 __all__ = [
     "memory_efficient_attention", "attention_packed", "attention_packed_fp8",
     "attention_packed_backward", "backward_workspace_size", "decode_splitkv", "decode_paged",
-    "decode_splitkv_noalloc", "decode_workspace_size", "wait_selftest", "alibi_slopes",
+    "decode_splitkv_noalloc", "decode_workspace_size", "decode_tree_paged",
+    "decode_tree_workspace_size", "tree_mask", "block_key_bounds", "select_blocks",
+    "decode_paged_selected", "decode_selected_workspace_size", "decode_paged_weights",
+    "decode_weights_workspace_size", "attention_packed_weights", "evict_paged", "wait_selftest",
+    "alibi_slopes",
     "BlockDiagonalMask", "BlockDiagonalCausalMask", "LowerTriangularMask", "device_error",
     "set_wait_timeout_ns", "MeaError", "library_path",
 ]
@@ -384,6 +393,364 @@ def decode_splitkv_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         int(max_seqlen_k), hq, hkv, d, float(scale), _lib.MEA_MASK_CAUSAL, _ptr(alibi_slopes),
         _dtype_code(q.dtype), int(split_keys), _stream(q.device))
     _lib.check(rc, "mea_decode_splitkv_noalloc")
+    return out, lse
+
+
+# ------------------------------------------------------------------------------------------
+# Operators on a paged K/V cache beside the plain decode.
+# ------------------------------------------------------------------------------------------
+def _check_paged(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor],
+                 block_table: torch.Tensor, cu_seqlens_k: torch.Tensor,
+                 q: Optional[torch.Tensor] = None):
+    """A cache ``[num_blocks, block_size, Hkv, D]`` with its block table and key counts: contiguous,
+    on one GPU, and, with ``q [rows, Hq, D]``, of its dtype and head dim. (A cache is never copied
+    here to make it contiguous.) Returns the block table and the prefix sums, contiguous."""
+    dev = k_cache.device
+    if not k_cache.is_cuda:
+        raise MeaError(_lib.MEA_ERR_DEVICE, "tensors must live on the GPU")
+    if k_cache.dim() != 4 or not k_cache.is_contiguous() or (
+            v_cache is not None and (v_cache.shape != k_cache.shape
+                                     or not v_cache.is_contiguous())):
+        raise MeaError(_lib.MEA_ERR_SHAPE,
+                       "caches must be contiguous [num_blocks, block_size, Hkv, D] tensors")
+    if v_cache is not None and (v_cache.dtype != k_cache.dtype or v_cache.device != dev):
+        raise MeaError(_lib.MEA_ERR_DTYPE, "k_cache and v_cache must share one dtype and GPU")
+    if q is not None:
+        if q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
+            raise MeaError(_lib.MEA_ERR_SHAPE, "q must be [rows, Hq, D] with the cache's D")
+        if q.dtype != k_cache.dtype:
+            raise MeaError(_lib.MEA_ERR_DTYPE, "q and the cache must share one dtype")
+        if q.device != dev:
+            raise MeaError(_lib.MEA_ERR_DEVICE, f"q must be a CUDA tensor on {dev}")
+    if block_table.dim() != 2 or block_table.dtype != torch.int32:
+        raise MeaError(_lib.MEA_ERR_SHAPE, "block_table must be int32 [n_seqs, max_blocks]")
+    _on_device(dev, block_table=block_table)
+    cu = _check_cu("cu_seqlens_k", cu_seqlens_k, block_table.shape[0] + 1, dev)
+    return block_table.contiguous(), cu
+
+
+def _launch(device: torch.device, name: str, *args) -> None:
+    """Calls library function ``name`` with ``device`` current and its current stream as the last
+    argument (a launch goes to the current device, whichever the tensors live on)."""
+    fn = getattr(_lib.load(), name)
+    if torch.cuda.current_device() == device.index:
+        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
+    if rc != _lib.MEA_OK:
+        raise MeaError(rc, name)
+
+
+def _slopes_for(alibi_slopes: Optional[torch.Tensor], hq: int, device: torch.device):
+    if alibi_slopes is None:
+        return None
+    if tuple(alibi_slopes.shape) != (hq,):
+        raise MeaError(_lib.MEA_ERR_SHAPE, f"alibi_slopes must be [{hq}]")
+    return alibi_slopes.to(device=device, dtype=torch.float32).contiguous()
+
+
+def _output(name, t, shape, dtype, device) -> torch.Tensor:
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _check_buffer(name, t, shape, dtype, device)
+
+
+def _check_weights(name: str, t: torch.Tensor, n: int, hkv: int, max_k: int,
+                   device: torch.device) -> torch.Tensor:
+    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != hkv or t.shape[2] < max_k \
+            or t.dtype != torch.float32 or t.device != device or not t.is_contiguous():
+        raise MeaError(_lib.MEA_ERR_SHAPE,
+                       f"{name} must be a contiguous float32 [{n}, {hkv}, >= {max_k}] tensor on "
+                       f"{device}")
+    return t
+
+
+def block_key_bounds(k_cache: torch.Tensor, block_table: torch.Tensor,
+                     cu_seqlens_k: torch.Tensor, max_seqlen_k: int,
+                     first_key: Optional[torch.Tensor] = None,
+                     bounds: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The least and greatest key of every cache block, per KV head and column, over the slots that
+    hold a key: ``bounds [num_blocks, Hkv, 2, D]`` in the cache's dtype, what
+    :func:`select_blocks` reads. With ``first_key`` (int32 ``[n_seqs]``) only the blocks that hold a
+    request's keys from ``first_key[b]`` on are done: after a decode step, its newest key's block.
+    Blocks in no request's table are left as they were (zeros when ``bounds`` is made here)."""
+    table, cu = _check_paged(k_cache, None, block_table, cu_seqlens_k)
+    nb, bs, hkv, d = k_cache.shape
+    dev = k_cache.device
+    n = table.shape[0]
+    if first_key is not None:
+        first_key = _check_cu("first_key", first_key, n, dev)
+    if bounds is None:
+        bounds = torch.zeros((nb, hkv, 2, d), dtype=k_cache.dtype, device=dev)
+    else:
+        _check_buffer("bounds", bounds, (nb, hkv, 2, d), k_cache.dtype, dev)
+    _launch(
+        dev, "mea_block_key_bounds",
+        _ptr(k_cache), _ptr(table), _ptr(cu), _ptr(first_key), _ptr(bounds), n, nb, bs,
+        table.shape[1], int(max_seqlen_k), hkv, d, _dtype_code(k_cache.dtype))
+    return bounds
+
+
+def select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tensor,
+                  cu_seqlens_k: torch.Tensor, max_seqlen_k: int, block_size: int, n_select: int,
+                  n_first: int = 1, n_last: int = 1,
+                  selected: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The ``n_select`` cache blocks that each (request, KV head) attends to: its first ``n_first``,
+    its last ``n_last``, and of the others those whose key ranges (:func:`block_key_bounds`) allow
+    the greatest sum over the group's heads of ``q . k``. Returns int32
+    ``[n_seqs, Hkv, n_select]``, block indices within the request in ascending order, -1 after the
+    last one when the request has fewer blocks. Equal scores: the lower index."""
+    if q.dim() != 3 or bounds.dim() != 4 or bounds.shape[2] != 2 \
+            or bounds.shape[3] != q.shape[2]:
+        raise MeaError(_lib.MEA_ERR_SHAPE, "q [n_seqs, Hq, D], bounds [num_blocks, Hkv, 2, D]")
+    if not q.is_cuda:
+        raise MeaError(_lib.MEA_ERR_DEVICE, "tensors must live on the GPU")
+    if q.dtype != bounds.dtype:
+        raise MeaError(_lib.MEA_ERR_DTYPE, "q and bounds must share one dtype")
+    dev = q.device
+    _on_device(dev, bounds=bounds, block_table=block_table)
+    n, hq, d = q.shape
+    nb, hkv = bounds.shape[:2]
+    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != n:
+        raise MeaError(_lib.MEA_ERR_SHAPE, "block_table must be int32 [n_seqs, max_blocks]")
+    if not bounds.is_contiguous():
+        raise MeaError(_lib.MEA_ERR_SHAPE, "bounds must be contiguous")
+    q, block_table = q.contiguous(), block_table.contiguous()
+    cu = _check_cu("cu_seqlens_k", cu_seqlens_k, n + 1, dev)
+    selected = _output("selected", selected, (n, hkv, int(n_select)), torch.int32, dev)
+    _launch(
+        dev, "mea_select_blocks",
+        _ptr(q), _ptr(bounds), _ptr(block_table), _ptr(cu), _ptr(selected), n, nb, int(block_size),
+        block_table.shape[1], int(max_seqlen_k), hq, hkv, d, int(n_select), int(n_first),
+        int(n_last), _dtype_code(q.dtype))
+    return selected
+
+
+def decode_selected_workspace_size(n_seqs: int, n_select: int, block_size: int, n_heads_q: int,
+                                   n_heads_kv: int, head_dim: int, split_keys: int = 0) -> int:
+    return int(_lib.load().mea_decode_selected_workspace_size(
+        n_seqs, n_select, block_size, n_heads_q, n_heads_kv, head_dim, split_keys))
+
+
+def decode_paged_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                          block_table: torch.Tensor, cu_seqlens_k: torch.Tensor,
+                          selected: torch.Tensor, alibi_slopes: Optional[torch.Tensor] = None,
+                          scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
+                          split_keys: int = 0, out: Optional[torch.Tensor] = None,
+                          lse: Optional[torch.Tensor] = None):
+    """:func:`decode_paged` over the blocks in ``selected`` (:func:`select_blocks`) only. Entries may
+    be in any order; one below 0 or past the request's blocks names no keys, a block listed twice
+    counts twice. Returns ``(out [n_seqs, Hq, D], lse [Hq, n_seqs])``."""
+    table, cu = _check_paged(k_cache, v_cache, block_table, cu_seqlens_k, q)
+    q = q.contiguous()
+    n, hq, d = q.shape
+    nb, bs, hkv, _ = k_cache.shape
+    dev = q.device
+    if n != table.shape[0] or selected.dtype != torch.int32 or selected.dim() != 3 \
+            or tuple(selected.shape[:2]) != (n, hkv):
+        raise MeaError(_lib.MEA_ERR_SHAPE, f"selected must be int32 [{n}, {hkv}, n_select]")
+    _on_device(dev, selected=selected)
+    selected = selected.contiguous()
+    sel = selected.shape[2]
+    if workspace is None:
+        workspace = torch.empty(decode_selected_workspace_size(n, sel, bs, hq, hkv, d, split_keys),
+                                dtype=torch.uint8, device=dev)
+    out = _output("out", out, (n, hq, d), q.dtype, dev)
+    lse = _output("lse", lse, (hq, n), torch.float32, dev)
+    slopes = _slopes_for(alibi_slopes, hq, dev)
+    _launch(
+        dev, "mea_decode_selected",
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(cu), _ptr(selected), _ptr(out),
+        _ptr(lse), n, nb, bs, table.shape[1], sel, hq, hkv, d, 1.0 / math.sqrt(d) if scale is None
+        else float(scale), _ptr(slopes), _dtype_code(q.dtype), _ptr(workspace),
+        _check_workspace(workspace, dev), int(split_keys))
+    return out, lse
+
+
+def decode_weights_workspace_size(n_seqs: int, total_k: int, n_heads_q: int, n_heads_kv: int,
+                                  head_dim: int, split_keys: int = 0) -> int:
+    return int(_lib.load().mea_decode_weights_workspace_size(n_seqs, total_k, n_heads_q,
+                                                             n_heads_kv, head_dim, split_keys))
+
+
+def decode_paged_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                         block_table: torch.Tensor, cu_seqlens_k: torch.Tensor, max_seqlen_k: int,
+                         weights: torch.Tensor, prev_weights: Optional[torch.Tensor] = None,
+                         alibi_slopes: Optional[torch.Tensor] = None,
+                         scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
+                         split_keys: int = 0, total_k_bound: Optional[int] = None,
+                         out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+    """:func:`decode_paged` that also writes each key's attention weight, summed over the heads of
+    its KV group and added to ``prev_weights`` (None: zeros; ``weights`` itself: accumulate in
+    place), to ``weights`` fp32 ``[n_seqs, Hkv, >= max_seqlen_k]``; entries past a request's keys
+    are left as they were. Returns ``(out [n_seqs, Hq, D], lse [Hq, n_seqs], weights)``."""
+    table, cu = _check_paged(k_cache, v_cache, block_table, cu_seqlens_k, q)
+    q = q.contiguous()
+    n, hq, d = q.shape
+    nb, bs, hkv, _ = k_cache.shape
+    dev = q.device
+    if n != table.shape[0]:
+        raise MeaError(_lib.MEA_ERR_SHAPE, "block_table must have a row per request")
+    _check_weights("weights", weights, n, hkv, int(max_seqlen_k), dev)
+    if prev_weights is not None:
+        _check_buffer("prev_weights", prev_weights, weights.shape, torch.float32, dev)
+    total = int(total_k_bound) if total_k_bound is not None else nb * bs
+    if workspace is None:
+        workspace = torch.empty(decode_weights_workspace_size(n, total, hq, hkv, d, split_keys),
+                                dtype=torch.uint8, device=dev)
+    out = _output("out", out, (n, hq, d), q.dtype, dev)
+    lse = _output("lse", lse, (hq, n), torch.float32, dev)
+    slopes = _slopes_for(alibi_slopes, hq, dev)
+    _launch(
+        dev, "mea_decode_weights",
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(cu), _ptr(out), _ptr(lse),
+        _ptr(weights), _ptr(prev_weights), weights.shape[2], n, nb, bs, table.shape[1], total,
+        int(max_seqlen_k), hq, hkv, d, 1.0 / math.sqrt(d) if scale is None else float(scale),
+        _ptr(slopes), _dtype_code(q.dtype), _ptr(workspace), _check_workspace(workspace, dev),
+        int(split_keys))
+    return out, lse, weights
+
+
+def attention_packed_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor,
+                             cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor,
+                             max_seqlen_q: int, max_seqlen_k: int, causal: bool = False,
+                             alibi_slopes: Optional[torch.Tensor] = None,
+                             scale: Optional[float] = None, last_queries: int = 0,
+                             weights: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The attention weight that a packed batch's queries put on its keys, for
+    :func:`attention_packed` called with the same arguments (``lse`` is its result): ``weights`` fp32
+    ``[n_seqs, Hkv, >= max_seqlen_k]``, summed over the heads of a KV group and over the queries
+    (``last_queries`` > 0: each segment's last ones only). Entries past a segment's keys are left as
+    they were (zeros when ``weights`` is made here)."""
+    if q.dim() != 3 or k.dim() != 3 or k.shape[2] != q.shape[2]:
+        raise MeaError(_lib.MEA_ERR_SHAPE, "q [T_q, Hq, D], k [T_k, Hkv, D]")
+    if q.dtype != k.dtype:
+        raise MeaError(_lib.MEA_ERR_DTYPE, "q and k must share one dtype")
+    if not q.is_cuda:
+        raise MeaError(_lib.MEA_ERR_DEVICE, "tensors must live on the GPU")
+    dev = q.device
+    _on_device(dev, k=k, lse=lse)
+    q, k, lse = q.contiguous(), k.contiguous(), lse.contiguous()
+    tq, hq, d = q.shape
+    tk, hkv, _ = k.shape
+    if tuple(lse.shape) != (hq, tq) or lse.dtype != torch.float32:
+        raise MeaError(_lib.MEA_ERR_SHAPE, f"lse must be float32 [{hq}, {tq}]")
+    n = cu_seqlens_q.numel() - 1
+    cu_q = _check_cu("cu_seqlens_q", cu_seqlens_q, n + 1, dev)
+    cu_k = _check_cu("cu_seqlens_k", cu_seqlens_k, n + 1, dev)
+    if weights is None:
+        weights = torch.zeros((n, hkv, int(max_seqlen_k)), dtype=torch.float32, device=dev)
+    else:
+        _check_weights("weights", weights, n, hkv, int(max_seqlen_k), dev)
+    slopes = _slopes_for(alibi_slopes, hq, dev)
+    _launch(
+        dev, "mea_attention_weights",
+        _ptr(q), _ptr(k), _ptr(lse), _ptr(cu_q), _ptr(cu_k), _ptr(weights), weights.shape[2], n, tq,
+        tk, int(max_seqlen_q), int(max_seqlen_k), hq, hkv, d, 1.0 / math.sqrt(d) if scale is None
+        else float(scale), _lib.MEA_MASK_CAUSAL if causal else _lib.MEA_MASK_NONE, _ptr(slopes),
+        int(last_queries), _dtype_code(q.dtype))
+    return weights
+
+
+def evict_paged(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                cu_seqlens_k: torch.Tensor, max_seqlen_k: int, weights: torch.Tensor, n_keep: int,
+                n_recent: int, out_table: torch.Tensor,
+                out_k_cache: Optional[torch.Tensor] = None,
+                out_v_cache: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None,
+                out_weights: Optional[torch.Tensor] = None,
+                out_cu_seqlens_k: Optional[torch.Tensor] = None):
+    """Keeps ``n_keep`` keys of each (request, KV head): the last ``n_recent`` and, of the others,
+    those with the greatest ``weights`` (equal ones: the lower index). Their K and V rows are
+    copied, in order, to the blocks of ``out_table`` (int32 ``[n_seqs, max_out_blocks]``), which
+    are blocks of ``out_k_cache`` / ``out_v_cache`` (None: of the same caches, and then none that a
+    request still reads from). Returns ``(kept [n_seqs, Hkv, n_keep] int32, out_weights of the same
+    shape, out_cu_seqlens_k [n_seqs + 1])``: the kept keys' indices (then -1) and weights (then 0)
+    and the new prefix sums. Afterwards a slot holds another token's key for each head, so ALiBi no
+    longer applies."""
+    table, cu = _check_paged(k_cache, v_cache, block_table, cu_seqlens_k)
+    nb, bs, hkv, d = k_cache.shape
+    dev = k_cache.device
+    n = table.shape[0]
+    _check_weights("weights", weights, n, hkv, int(max_seqlen_k), dev)
+    out_k_cache = k_cache if out_k_cache is None else out_k_cache
+    out_v_cache = v_cache if out_v_cache is None else out_v_cache
+    for name, t in (("out_k_cache", out_k_cache), ("out_v_cache", out_v_cache)):
+        _check_buffer(name, t, (out_k_cache.shape[0], bs, hkv, d), k_cache.dtype, dev)
+    if out_table.dtype != torch.int32 or out_table.dim() != 2 or out_table.shape[0] != n:
+        raise MeaError(_lib.MEA_ERR_SHAPE, "out_table must be int32 [n_seqs, max_out_blocks]")
+    _on_device(dev, out_table=out_table)
+    out_table = out_table.contiguous()
+    n_keep = int(n_keep)
+    kept = _output("kept", kept, (n, hkv, n_keep), torch.int32, dev)
+    out_weights = _output("out_weights", out_weights, (n, hkv, n_keep), torch.float32, dev)
+    out_cu = _output("out_cu_seqlens_k", out_cu_seqlens_k, (n + 1,), torch.int32, dev)
+    _launch(
+        dev, "mea_evict_paged",
+        _ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(cu), _ptr(weights), weights.shape[2],
+        _ptr(out_k_cache), _ptr(out_v_cache), _ptr(out_table), _ptr(kept), _ptr(out_weights),
+        _ptr(out_cu), n, nb, out_k_cache.shape[0], bs, table.shape[1], out_table.shape[1],
+        int(max_seqlen_k), hkv, d, n_keep, int(n_recent), _dtype_code(k_cache.dtype))
+    return kept, out_weights, out_cu
+
+
+def tree_mask(parents: Sequence[Sequence[int]], device=None) -> torch.Tensor:
+    """The mask of :func:`decode_tree_paged` for drafted trees: ``parents[b][i]`` is the index of
+    drafted token i's parent among request b's drafted tokens (less than i), or -1 for a child of
+    the context. int32 ``[sum of lengths, words]``: a token sees its ancestors and itself."""
+    words = max(1, max(((len(t) + 31) // 32 for t in parents), default=1))
+    rows = []
+    for t in parents:
+        seen: List[int] = []
+        for i, par in enumerate(t):
+            if not -1 <= par < i:
+                raise ValueError(f"parent {par} of token {i} must be -1 or an earlier token")
+            seen.append((seen[par] if par >= 0 else 0) | (1 << i))
+        rows += seen
+    flat = [[(m >> (32 * w)) & 0xFFFFFFFF for w in range(words)] for m in rows]
+    t64 = torch.tensor(flat, dtype=torch.int64).reshape(len(rows), words)
+    return torch.where(t64 >= 1 << 31, t64 - (1 << 32), t64).to(torch.int32).to(device)
+
+
+def decode_tree_workspace_size(n_heads_q: int, n_heads_kv: int, head_dim: int) -> int:
+    return int(_lib.load().mea_decode_tree_workspace_size(n_heads_q, n_heads_kv, head_dim))
+
+
+def decode_tree_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                      block_table: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                      cu_seqlens_k: torch.Tensor, max_seqlen_q: int, max_seqlen_k: int,
+                      tree_mask: torch.Tensor, alibi_slopes: Optional[torch.Tensor] = None,
+                      scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
+    """Attention of drafted tokens over a paged cache: q ``[T_q, Hq, D]`` holds request b's drafted
+    tokens at rows ``cu_seqlens_q[b]..``; their keys and values are the last of the request's
+    ``cu_seqlens_k`` cached ones. A token attends to every key before the drafted ones and to
+    drafted token j when bit j % 32 of word j / 32 of its ``tree_mask`` row (int32 ``[T_q, words]``,
+    :func:`tree_mask`) is set. ALiBi positions are the depths in the tree. Returns
+    ``(out [T_q, Hq, D], lse [Hq, T_q])``."""
+    table, cu_k = _check_paged(k_cache, v_cache, block_table, cu_seqlens_k, q)
+    q = q.contiguous()
+    tq, hq, d = q.shape
+    nb, bs, hkv, _ = k_cache.shape
+    dev = q.device
+    n = table.shape[0]
+    cu_q = _check_cu("cu_seqlens_q", cu_seqlens_q, n + 1, dev)
+    if tree_mask.dtype != torch.int32 or tree_mask.dim() != 2 or tree_mask.shape[0] != tq:
+        raise MeaError(_lib.MEA_ERR_SHAPE, f"tree_mask must be int32 [{tq}, words]")
+    _on_device(dev, tree_mask=tree_mask)
+    tree_mask = tree_mask.contiguous()
+    if workspace is None:
+        workspace = torch.empty(decode_tree_workspace_size(hq, hkv, d), dtype=torch.uint8,
+                                device=dev)
+    out = _output("out", out, (tq, hq, d), q.dtype, dev)
+    lse = _output("lse", lse, (hq, tq), torch.float32, dev)
+    slopes = _slopes_for(alibi_slopes, hq, dev)
+    _launch(
+        dev, "mea_decode_tree",
+        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(cu_q), _ptr(cu_k), _ptr(tree_mask),
+        _ptr(out), _ptr(lse), n, tq, int(max_seqlen_q), int(max_seqlen_k), tree_mask.shape[1], nb,
+        bs, table.shape[1], hq, hkv, d, 1.0 / math.sqrt(d) if scale is None else float(scale),
+        _ptr(slopes), _dtype_code(q.dtype), _ptr(workspace), _check_workspace(workspace, dev))
     return out, lse
 
 

@@ -6,6 +6,8 @@ import hashlib
 import os
 import shutil
 import subprocess
+import tempfile
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -16,7 +18,7 @@ INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
     "-O3", "-lineinfo", "-std=c++17",
-    "-Xcompiler", "-fPIC", "-shared",
+    "-Xcompiler", "-fPIC",
 ]
 
 
@@ -29,6 +31,7 @@ def _nvcc() -> str:
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cuh"))
+                  + glob.glob(os.path.join(CSRC, "*.h"))
                   + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
@@ -52,20 +55,29 @@ def up_to_date() -> bool:
         return f.read().strip() == source_hash()
 
 
-def build_library(force: bool = False, verbose: bool = False) -> str:
-    """Compiles csrc/mea_api.cu (which includes the kernels) into libmea.so; returns its path."""
-    if not force and up_to_date():
-        return LIB
-    tmp = LIB + ".tmp"
-    cmd = [_nvcc(), *NVCC_FLAGS, "-o", tmp, os.path.join(CSRC, "mea_api.cu")]
+def _run(cmd, verbose: bool) -> None:
     if verbose:
-        cmd.insert(1, "-Xptxas=-v")
         print(" ".join(cmd))
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"nvcc failed ({res.returncode}):\n{res.stdout}\n{res.stderr}")
     if verbose:
         print(res.stderr)
+
+
+def build_library(force: bool = False, verbose: bool = False) -> str:
+    """Compiles every csrc/*.cu (side by side) and links them into libmea.so; returns its path."""
+    if not force and up_to_date():
+        return LIB
+    units = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
+    tmp = LIB + ".tmp"
+    with tempfile.TemporaryDirectory() as work:
+        objs = [os.path.join(work, os.path.basename(u) + ".o") for u in units]
+        flags = [*NVCC_FLAGS, "-Xptxas=-v"] if verbose else NVCC_FLAGS
+        with ThreadPoolExecutor(len(units)) as pool:
+            list(pool.map(lambda uo: _run([_nvcc(), *flags, "-c", "-o", uo[1], uo[0]], verbose),
+                          zip(units, objs)))
+        _run([_nvcc(), *NVCC_FLAGS, "-shared", "-o", tmp, *objs], verbose)
     os.replace(tmp, LIB)
     with open(STAMP, "w") as f:
         f.write(source_hash() + "\n")

@@ -1,0 +1,478 @@
+// cache_sm100.cuh — operators on a paged K/V cache beside the attention that reads it, for
+// sm_100a: the blocks' key ranges, the choice of the blocks a query attends to, and the removal of
+// the keys with the least attention weight.
+//
+// Cache layout throughout: K and V are [num_blocks, block_size, Hkv, D] in 16 bits; key t of
+// request b lives in block block_table[b, t / block_size], slot t % block_size. Ids outside
+// [0, num_blocks) are skipped, never dereferenced.
+#pragma once
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <type_traits>
+
+#include "ptx.cuh"
+
+namespace mea {
+
+template <bool BF16>
+using Half2 = typename std::conditional<BF16, __nv_bfloat162, __half2>::type;
+template <bool BF16>
+using Half1 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+
+// ------------------------------------------------------------------------------------------
+// Key ranges: lo[blk, g, d] = min over the block's existing slots of K[slot, g, d], hi = max.
+//
+// Bound by reading K once (it writes 2 / block_size of what it reads). A thread owns 8 columns (16
+// bytes) of one block's rows and walks its slots, so that a warp reads whole rows; eight slots are
+// in flight per thread. Nothing is exchanged between threads.
+// ------------------------------------------------------------------------------------------
+struct BoundsParams {
+  const void* k;
+  void* bounds;  // [num_blocks, hkv, 2, D]
+  const int32_t* block_table;
+  const int32_t* cu_k;
+  const int32_t* first_key;  // [n_seqs] or null: only blocks that hold keys >= first_key[b]
+  int num_blocks, block_size, max_blocks, hkv, dh;
+};
+
+template <bool BF16>
+__global__ void __launch_bounds__(256) mea_key_bounds_kernel(const BoundsParams p) {
+  const int b = blockIdx.y;
+  const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
+  const int nblk = min((L + p.block_size - 1) / p.block_size, p.max_blocks);
+  const int first = p.first_key ? max(__ldg(p.first_key + b), 0) / p.block_size : 0;
+  const int row16 = p.hkv * p.dh / 8;  // 16-byte pieces of a slot's row over all heads
+  const long long n = static_cast<long long>(nblk - first) * row16;
+  const uint4* k = static_cast<const uint4*>(p.k);
+  uint4* out = static_cast<uint4*>(p.bounds);
+  for (long long u = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x; u < n;
+       u += static_cast<long long>(gridDim.x) * blockDim.x) {
+    const int jj = static_cast<int>(u / row16);
+    const int j = first + jj;
+    const int ch = static_cast<int>(u - static_cast<long long>(jj) * row16);
+    const int id = __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + j);
+    if (id < 0 || id >= p.num_blocks) continue;
+    const int ns = min(p.block_size, L - j * p.block_size);
+    const uint4* src = k + static_cast<size_t>(id) * p.block_size * row16 + ch;
+    using H2 = Half2<BF16>;
+    H2 lo[4], hi[4];
+    uint4 v = __ldg(src);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lo[i] = hi[i] = reinterpret_cast<const H2*>(&v)[i];
+    for (int t = 1; t < ns; t += 8) {
+      uint4 w[8];
+      // (slots past the last one repeat it)
+#pragma unroll
+      for (int q = 0; q < 8; ++q) w[q] = __ldg(src + static_cast<size_t>(min(t + q, ns - 1)) * row16);
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const H2 x = reinterpret_cast<const H2*>(&w[q])[i];
+          lo[i] = __hmin2_nan(lo[i], x);
+          hi[i] = __hmax2_nan(hi[i], x);
+        }
+      }
+    }
+    const int d8 = p.dh / 8;
+    const int g = ch / d8, c = ch - g * d8;
+    uint4* dst = out + (static_cast<size_t>(id) * p.hkv + g) * 2 * d8 + c;
+    dst[0] = *reinterpret_cast<uint4*>(lo);
+    dst[d8] = *reinterpret_cast<uint4*>(hi);
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// The k largest of n 32-bit keys by one CTA: radix selection, 8 bits a pass from the top. Returns
+// the key T of the k-th largest and in `ties` how many of the keys equal to T belong to the k
+// (the caller takes the lowest indices of them). 1 <= k <= n. `hist` holds 256 + 2 ints.
+// ------------------------------------------------------------------------------------------
+// Order-preserving image of an fp32 value (as unsigned; -0 equals +0). NaN ranks above all.
+__device__ __forceinline__ uint32_t rank_key(float x) {
+  if (x != x) return 0xFFFFFFFEu;
+  const uint32_t u = __float_as_uint(x + 0.f);
+  return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+constexpr uint32_t kRankAlways = 0xFFFFFFFFu;  // ranks above every value
+
+template <class Get>
+__device__ __forceinline__ uint32_t radix_select(Get get, int n, int k, int* hist, int& ties) {
+  const int tid = threadIdx.x, nt = blockDim.x;
+  uint32_t prefix = 0;
+  int need = k;
+  for (int shift = 24; shift >= 0; shift -= 8) {
+    for (int i = tid; i < 256; i += nt) hist[i] = 0;
+    __syncthreads();
+    const uint32_t high = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+    for (int i = tid; i < n; i += nt) {
+      const uint32_t x = get(i);
+      if ((x & high) == prefix) atomicAdd(&hist[(x >> shift) & 255u], 1);
+    }
+    __syncthreads();
+    // Warp 0: the bin, counted from the top, in which the need-th key falls.
+    if (tid < 32) {
+      int c[8], sum = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        c[i] = hist[255 - (tid * 8 + i)];
+        sum += c[i];
+      }
+      int incl = sum;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (tid >= off) incl += y;
+      }
+      int above = incl - sum;
+      if (above < need && need <= incl) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (above < need && need <= above + c[i]) {
+            hist[256] = 255 - (tid * 8 + i);
+            hist[257] = above;
+          }
+          above += c[i];
+        }
+      }
+    }
+    __syncthreads();
+    prefix |= static_cast<uint32_t>(hist[256]) << shift;
+    need -= hist[257];
+    __syncthreads();
+  }
+  ties = need;
+  return prefix;
+}
+
+// Writes the indices of the keys above T, and of the first `ties` keys equal to T, in ascending
+// order through put(place, index). `scan` holds 2 * 32 ints.
+template <class Get, class Put>
+__device__ __forceinline__ void compact_selected(Get get, Put put, int n, uint32_t T, int ties,
+                                                 int* scan) {
+  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
+  const int nw = nt >> 5;
+  const unsigned below = (1u << lane) - 1u;
+  int base_gt = 0, base_eq = 0;  // keys above / equal before this round's range
+  for (int i0 = 0; i0 < n; i0 += nt) {
+    const int i = i0 + tid;
+    const uint32_t x = i < n ? get(i) : 0u;
+    const bool gt = i < n && x > T, eq = i < n && x == T;
+    const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
+    if (lane == 0) {
+      scan[warp] = __popc(bg);
+      scan[32 + warp] = __popc(be);
+    }
+    __syncthreads();
+    int pg = base_gt + __popc(bg & below), pe = base_eq + __popc(be & below);
+    for (int w = 0; w < nw; ++w) {
+      const int cg = scan[w], ce = scan[32 + w];
+      if (w < warp) {
+        pg += cg;
+        pe += ce;
+      }
+      base_gt += cg;
+      base_eq += ce;
+    }
+    if (gt || (eq && pe < ties)) put(pg + min(pe, ties), i);
+    __syncthreads();
+  }
+}
+
+// ------------------------------------------------------------------------------------------
+// Choice of blocks. For every key k of block j and the R query heads q_h of its KV head,
+//     sum_h q_h . k <= sum_d up[d] hi[j, d] + down[d] lo[j, d],
+//     up = sum_h max(q_h, 0),  down = sum_h min(q_h, 0)       (each term bounds its own product),
+// which is the block's score: one dot product of length 2 D, whatever the group's size, because
+// the bound of a sum of heads is linear in (up, down). The scores are summed in 64 bits and rounded
+// to 32 once: then the order of summation does not show in the choice.
+//
+// Bound by reading the ranges (4 D bytes a block and head). A cluster of CTAs serves one (request,
+// KV head): each CTA's warps score a share of its blocks (a warp reads a block's two rows with
+// one 16-byte load a lane, eight blocks in flight, and adds the eight sums up together) and leave
+// the rank keys in the first CTA's shared memory, which then selects.
+// ------------------------------------------------------------------------------------------
+struct SelectParams {
+  const void* q;       // [n_seqs, hq, D]
+  const void* bounds;  // [num_blocks, hkv, 2, D]
+  const int32_t* block_table;
+  const int32_t* cu_k;
+  int32_t* selected;   // [n_seqs, hkv, n_select]
+  int num_blocks, block_size, max_blocks, hq, hkv, dh, n_select, n_first, n_last;
+  int max_live;        // bound on a request's blocks: rank keys in shared memory
+};
+
+constexpr int kSelThreads = 512;
+
+template <bool BF16>
+__device__ __forceinline__ float half_f32(uint32_t w, int i) {
+  const Half2<BF16> h = *reinterpret_cast<const Half2<BF16>*>(&w);
+  if constexpr (BF16)
+    return i ? __high2float(h) : __low2float(h);
+  else
+    return i ? __high2float(h) : __low2float(h);
+}
+
+// PIECES: 16-byte pieces of a block's two rows per lane (1 up to head dim 128, 2 above).
+template <bool BF16, int PIECES>
+__global__ void __launch_bounds__(kSelThreads) mea_select_blocks_kernel(const SelectParams p) {
+  namespace cg = cooperative_groups;
+  auto cluster = cg::this_cluster();
+  const int cs = static_cast<int>(cluster.num_blocks());
+  const int cr = static_cast<int>(cluster.block_rank());
+  const int pair = blockIdx.x / cs;
+  const int b = pair / p.hkv, g = pair - b * p.hkv;
+  const int R = p.hq / p.hkv;
+  extern __shared__ __align__(16) uint32_t s_keys[];
+  __shared__ double s_w[2 * 256];  // [lo half: down][hi half: up]
+  __shared__ int s_hist[258];
+  __shared__ int s_scan[64];
+  const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
+  const int nblk = min((L + p.block_size - 1) / p.block_size, min(p.max_blocks, p.max_live));
+  int32_t* out = p.selected + (static_cast<size_t>(b) * p.hkv + g) * p.n_select;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (nblk <= p.n_select) {  // every block (the whole cluster takes this branch)
+    if (cr == 0)
+      for (int i = tid; i < p.n_select; i += kSelThreads) out[i] = i < nblk ? i : -1;
+    return;
+  }
+  const Half1<BF16>* q =
+      static_cast<const Half1<BF16>*>(p.q) + (static_cast<size_t>(b) * p.hq + g * R) * p.dh;
+  for (int d = tid; d < p.dh; d += kSelThreads) {
+    double up = 0.0, down = 0.0;
+    for (int h = 0; h < R; ++h) {
+      const float x = static_cast<float>(q[static_cast<size_t>(h) * p.dh + d]);
+      up += x > 0.f ? x : 0.f;
+      down += x > 0.f ? 0.f : x;  // (a NaN goes here)
+    }
+    s_w[d] = down;
+    s_w[p.dh + d] = up;
+  }
+  // The first CTA's shared memory must be live before others write to it.
+  cluster.sync();
+  uint32_t* keys = cluster.map_shared_rank(s_keys, 0);
+  const int np = p.dh / 4;  // 16-byte pieces of a block's ranges
+  double w[PIECES][8];
+#pragma unroll
+  for (int c = 0; c < PIECES; ++c)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      w[c][i] = lane + 32 * c < np ? s_w[(lane + 32 * c) * 8 + i] : 0.0;
+  const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
+  const uint4* bounds = static_cast<const uint4*>(p.bounds);
+  constexpr int U = 8;  // blocks in flight per warp
+  const int warps = cs * (kSelThreads / 32);
+  for (int j0 = (cr * (kSelThreads / 32) + warp) * U; j0 < nblk; j0 += warps * U) {
+    const int my_id = (lane < U && j0 + lane < nblk) ? __ldg(row + j0 + lane) : -1;
+    uint4 v[U][PIECES];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int id = __shfl_sync(0xffffffffu, my_id, u);
+      const bool in = id >= 0 && id < p.num_blocks;
+      const uint4* src = bounds + (static_cast<size_t>(in ? id : 0) * p.hkv + g) * np;
+#pragma unroll
+      for (int c = 0; c < PIECES; ++c)
+        v[u][c] = (in && lane + 32 * c < np) ? __ldg(src + lane + 32 * c)
+                                             : make_uint4(0u, 0u, 0u, 0u);
+    }
+    double s[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      s[u] = 0.0;
+#pragma unroll
+      for (int c = 0; c < PIECES; ++c) {
+        const uint32_t x[4] = {v[u][c].x, v[u][c].y, v[u][c].z, v[u][c].w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          s[u] = fma(w[c][i], static_cast<double>(half_f32<BF16>(x[i >> 1], i & 1)), s[u]);
+      }
+    }
+    // Eight sums over the warp at once: each step halves how many a lane carries.
+#pragma unroll
+    for (int half = U / 2, off = 16; half >= 1; half >>= 1, off >>= 1) {
+      const bool hi = (lane & off) != 0;
+#pragma unroll
+      for (int u = 0; u < U / 2; ++u) {
+        if (u < half) {
+          const double give = hi ? s[u] : s[u + half];
+          const double keep = hi ? s[u + half] : s[u];
+          s[u] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+        }
+      }
+    }
+    // (now lanes that agree in bits 2..4 of their index carry the same block)
+    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
+    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
+    const int u = (lane >> 2);  // bit 4 chose the upper four, bit 3 the upper two, bit 2 the odd one
+    if ((lane & 3) == 0 && j0 + u < nblk) {
+      const int j = j0 + u;
+      const bool always = j < p.n_first || j >= nblk - p.n_last;
+      keys[j] = always ? kRankAlways : rank_key(static_cast<float>(s[0]));
+    }
+  }
+  cluster.sync();
+  if (cr != 0) return;
+  int ties = 0;
+  auto get = [&](int i) { return s_keys[i]; };
+  const uint32_t T = radix_select(get, nblk, p.n_select, s_hist, ties);
+  compact_selected(get, [&](int at, int i) { out[at] = i; }, nblk, T, ties, s_scan);
+}
+
+// ------------------------------------------------------------------------------------------
+// Eviction, first kernel: the keys of (request b, KV head g) that stay: its last n_recent and, of
+// the others, those with the largest weights, n_keep in all, in ascending order. One CTA per
+// pair; the rank keys stay in shared memory when they fit (bound by reading the weights once).
+// ------------------------------------------------------------------------------------------
+struct EvictParams {
+  const void* k;
+  const void* v;
+  void* k_out;
+  void* v_out;
+  const int32_t* block_table;
+  const int32_t* out_table;  // [n_seqs, max_out_blocks]
+  const int32_t* cu_k;
+  const float* weights;      // [n_seqs, hkv, w_stride]
+  float* out_weights;        // [n_seqs, hkv, n_keep]
+  int32_t* kept;             // [n_seqs, hkv, n_keep]
+  int32_t* out_cu;           // [n_seqs + 1]
+  long long w_stride;
+  int num_blocks, num_out_blocks, block_size, max_blocks, max_out_blocks, n_seqs, hkv, dh;
+  int n_keep, n_recent;
+  int smem_keys;             // rank keys that fit in shared memory
+};
+
+constexpr int kEvictThreads = 1024;
+
+// Keys of request b (never past the row of weights).
+__device__ __forceinline__ int evict_keys(const EvictParams& p, int b) {
+  const int L = max(__ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b), 0);
+  return p.w_stride < L ? static_cast<int>(p.w_stride) : L;
+}
+
+__global__ void __launch_bounds__(kEvictThreads) mea_evict_select_kernel(const EvictParams p) {
+  extern __shared__ __align__(16) uint32_t s_keys[];
+  __shared__ int s_hist[258];
+  __shared__ int s_scan[64];
+  const int g = blockIdx.x % p.hkv, b = blockIdx.x / p.hkv;
+  const int tid = threadIdx.x;
+  const int L = evict_keys(p, b);
+  // The new prefix sums: one warp of the first CTA.
+  if (blockIdx.x == 0 && tid < 32) {
+    int base = 0;
+    for (int i0 = 0; i0 < p.n_seqs; i0 += 32) {
+      const int i = i0 + tid;
+      int incl = i < p.n_seqs ? min(evict_keys(p, i), p.n_keep) : 0;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, incl, off);
+        if (tid >= off) incl += y;
+      }
+      if (i < p.n_seqs) p.out_cu[i + 1] = base + incl;
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (tid == 0) p.out_cu[0] = 0;
+  }
+  const size_t pair = static_cast<size_t>(b) * p.hkv + g;
+  const float* w = p.weights + pair * p.w_stride;
+  int32_t* kept = p.kept + pair * p.n_keep;
+  float* ow = p.out_weights + pair * p.n_keep;
+  if (L <= p.n_keep) {
+    for (int i = tid; i < p.n_keep; i += kEvictThreads) {
+      kept[i] = i < L ? i : -1;
+      ow[i] = i < L ? w[i] : 0.f;
+    }
+    return;
+  }
+  const int m = L - p.n_recent;       // keys that compete, for
+  const int k = p.n_keep - p.n_recent;  // this many places (k < m)
+  if (k > 0) {
+    auto put = [&](int at, int i) {
+      kept[at] = i;
+      ow[at] = w[i];
+    };
+    int ties = 0;
+    if (m <= p.smem_keys) {
+      for (int i = tid; i < m; i += kEvictThreads) s_keys[i] = rank_key(w[i]);
+      __syncthreads();
+      auto get = [&](int i) { return s_keys[i]; };
+      const uint32_t T = radix_select(get, m, k, s_hist, ties);
+      compact_selected(get, put, m, T, ties, s_scan);
+    } else {
+      auto get = [&](int i) { return rank_key(__ldg(w + i)); };
+      const uint32_t T = radix_select(get, m, k, s_hist, ties);
+      compact_selected(get, put, m, T, ties, s_scan);
+    }
+  }
+  for (int i = tid; i < p.n_recent; i += kEvictThreads) {
+    kept[k + i] = m + i;
+    ow[k + i] = w[m + i];
+  }
+}
+
+// Second kernel: key kept[i]'s K and V rows of KV head g go to slot i of the request's new blocks.
+// Bound by moving the rows once (read and write). A CTA takes 64 rows of one pair: it looks their
+// places up once, then every thread moves 16-byte pieces, eight loads in flight.
+constexpr int kEvictRows = 64;
+
+__global__ void __launch_bounds__(256) mea_evict_copy_kernel(const EvictParams p) {
+  __shared__ long long s_src[kEvictRows], s_dst[kEvictRows];  // 16-byte piece offsets, -1: none
+  const int tiles = (p.n_keep + kEvictRows - 1) / kEvictRows;
+  const long long item = blockIdx.x;
+  const int tile = static_cast<int>(item % tiles);
+  const long long pair = item / tiles;
+  const int g = static_cast<int>(pair % p.hkv), b = static_cast<int>(pair / p.hkv);
+  const int L = evict_keys(p, b);
+  const int n = min(min(L, p.n_keep) - tile * kEvictRows, kEvictRows);
+  if (n <= 0) return;
+  const int d8 = p.dh / 8;
+  if (threadIdx.x < kEvictRows) {
+    const int i = tile * kEvictRows + threadIdx.x;
+    long long src = -1, dst = -1;
+    if (threadIdx.x < n) {
+      const int t = __ldg(p.kept + static_cast<size_t>(pair) * p.n_keep + i);
+      const int js = t / p.block_size, jd = i / p.block_size;
+      if (js < p.max_blocks && jd < p.max_out_blocks) {
+        const int is = __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + js);
+        const int id = __ldg(p.out_table + static_cast<size_t>(b) * p.max_out_blocks + jd);
+        if (is >= 0 && is < p.num_blocks && id >= 0 && id < p.num_out_blocks) {
+          src = ((static_cast<long long>(is) * p.block_size + t % p.block_size) * p.hkv + g) * d8;
+          dst = ((static_cast<long long>(id) * p.block_size + i % p.block_size) * p.hkv + g) * d8;
+        }
+      }
+    }
+    s_src[threadIdx.x] = src;
+    s_dst[threadIdx.x] = dst;
+  }
+  __syncthreads();
+  const uint4* k = static_cast<const uint4*>(p.k);
+  const uint4* v = static_cast<const uint4*>(p.v);
+  uint4* ko = static_cast<uint4*>(p.k_out);
+  uint4* vo = static_cast<uint4*>(p.v_out);
+  const int total = n * 2 * d8;  // pieces: [row][K or V][d8]
+  for (int i0 = threadIdx.x; i0 < total; i0 += 256 * 8) {
+    uint4 x[8];
+    long long to[8];
+    bool is_v[8];
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const int i = i0 + u * 256;
+      to[u] = -1;
+      if (i < total) {
+        const int half = i / d8, c = i - half * d8;
+        const int row = half >> 1;
+        is_v[u] = (half & 1) != 0;
+        if (s_src[row] >= 0) {
+          x[u] = __ldcs((is_v[u] ? v : k) + s_src[row] + c);
+          to[u] = s_dst[row] + c;
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      if (to[u] >= 0) (is_v[u] ? vo : ko)[to[u]] = x[u];
+  }
+}
+
+}  // namespace mea

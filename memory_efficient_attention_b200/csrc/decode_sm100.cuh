@@ -22,6 +22,13 @@
 
 namespace mea {
 
+// What a split kernel reads besides attending to all keys of a request:
+//   DEC_ALL       nothing more;
+//   DEC_SELECTED  (paged) only the cache blocks that a list names for the (request, KV head);
+//   DEC_WEIGHTS   (paged) all keys, and every score goes to the workspace, so that the merge can
+//                 turn it into the key's attention weight once the row's log-sum-exp is known.
+enum : int { DEC_ALL = 0, DEC_SELECTED = 1, DEC_WEIGHTS = 2 };
+
 struct DecParams {
   const void* q;      // [n_seqs, hq, D]
   void* out;          // [n_seqs, hq, D]
@@ -48,6 +55,15 @@ struct DecParams {
   long long n_items;  // n_slots * n_hb
   float c1;           // scale * log2(e)
   unsigned long long timeout_ns;
+  // DEC_SELECTED
+  const int32_t* selected;  // [n_seqs, hq / R, n_select] block indices in the request, -1: none
+  int n_select;
+  int n_chunks;             // chunks per request, ceil(n_select * block_size / chunk)
+  // DEC_WEIGHTS
+  float* ws_s;              // [n_slots, hq, chunk] scores in log2 units
+  const float* prev;        // [n_seqs, hq / R, w_stride] or null
+  float* weights;           // [n_seqs, hq / R, w_stride]
+  long long w_stride;
 };
 
 // Shared-memory layout of a K (or V) stage: groups of 2^lay_log2 key rows, each group
@@ -133,12 +149,30 @@ __device__ __forceinline__ int dec_chunk_start(const int32_t* cu, int b, int chu
   return acc;
 }
 
+// Warp-cooperative: keys of chunk `key0` of the (request b, KV head g) list, up to the end of its
+// last entry that names a block (entries after that load and add nothing).
+__device__ __forceinline__ int dec_selected_keys(const DecParams& p, int b, int g, int key0) {
+  const int lane = threadIdx.x & 31;
+  const int e0 = key0 / p.block_size;
+  const int ne = min(p.chunk / p.block_size, p.n_select - e0);
+  const int32_t* list =
+      p.selected + (static_cast<size_t>(b) * (p.hq / p.R) + g) * p.n_select + e0;
+  int live = 0;
+  for (int i = lane; i < ne; i += 32)
+    if (__ldg(list + i) >= 0) live = i + 1;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    live = max(live, __shfl_xor_sync(0xffffffffu, live, off));
+  return live * p.block_size;
+}
+
 // PAGED: K/V live in a block cache [num_blocks, block_size, Hkv, D] addressed through a per-request
 // block table (4-D TMA maps) instead of a packed [T_k, Hkv, D] tensor (3-D maps).
-template <int D, bool BF16, bool ALIBI, bool PAGED = false>
+template <int D, bool BF16, bool ALIBI, bool PAGED = false, int MODE = DEC_ALL>
 __global__ void __launch_bounds__(160, 1)
     mea_decode_split_kernel(const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v, const DecParams p) {
+  static_assert(PAGED || MODE == DEC_ALL, "block lists and weights: paged caches");
   using C = DecCfg<D, PAGED>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -181,14 +215,23 @@ __global__ void __launch_bounds__(160, 1)
       const int cid = static_cast<int>(lin / p.n_hb);
       const int hb = static_cast<int>(lin - static_cast<long long>(cid) * p.n_hb);
       int b, c;
-      dec_find_chunk(p.cu_k, p.n_seqs, p.chunk, cid, b, c);
-      if (b < 0) break;  // flat chunk ids only grow along this CTA's sequence
+      if constexpr (MODE == DEC_SELECTED) {
+        b = cid / p.n_chunks;
+        c = cid - b * p.n_chunks;
+      } else {
+        dec_find_chunk(p.cu_k, p.n_seqs, p.chunk, cid, b, c);
+        if (b < 0) break;  // flat chunk ids only grow along this CTA's sequence
+      }
       const int k0 = __ldg(p.cu_k + b);
       const int L = __ldg(p.cu_k + b + 1) - k0;
       const int key0 = c * p.chunk;
-      const int nk = min(p.chunk, L - key0);
-      const int n_tiles = (nk + C::BK - 1) / C::BK;
       const int g = (hb * p.RB) / p.R;
+      int nk;
+      if constexpr (MODE == DEC_SELECTED)
+        nk = dec_selected_keys(p, b, g, key0);
+      else
+        nk = min(p.chunk, L - key0);
+      const int n_tiles = (nk + C::BK - 1) / C::BK;
       if constexpr (PAGED) {
         // Tile keys [kt, kt + 64) of request b come from `per` cache blocks: one box per block
         // and per (K or V, 64-column atom) for block sizes 16 and 32 (boxes of block_size rows
@@ -208,8 +251,15 @@ __global__ void __launch_bounds__(160, 1)
         const int my_v = (lane / apb) & 1;                 // K or V
         const int my_a = lane % apb;                       // 64-column atom (4-D)
         const bool issuer = lane < nbox;
+        const int32_t* list = nullptr;
+        if constexpr (MODE == DEC_SELECTED)
+          list = p.selected + (static_cast<size_t>(b) * (p.hq / p.R) + g) * p.n_select;
         auto block_id = [&](int t) {
-          const int j = (key0 + t * C::BK + my_i * bs) / bs;
+          int j = (key0 + t * C::BK + my_i * bs) / bs;
+          if constexpr (MODE == DEC_SELECTED) {
+            j = (issuer && t < n_tiles && j < p.n_select) ? __ldg(list + j) : -1;
+            return (j >= 0 && j < nblk) ? __ldg(row + j) : p.num_blocks;
+          }
           return (issuer && t < n_tiles && j < nblk) ? __ldg(row + j) : p.num_blocks;
         };
         // Block ids of tiles t .. t+3: each read is in flight for three tiles before its TMA
@@ -285,11 +335,20 @@ __global__ void __launch_bounds__(160, 1)
       const int cid = static_cast<int>(lin / p.n_hb);
       const int hb = static_cast<int>(lin - static_cast<long long>(cid) * p.n_hb);
       int b, c;
-      dec_find_chunk(p.cu_k, p.n_seqs, p.chunk, cid, b, c);
-      if (b < 0) break;
+      if constexpr (MODE == DEC_SELECTED) {
+        b = cid / p.n_chunks;
+        c = cid - b * p.n_chunks;
+      } else {
+        dec_find_chunk(p.cu_k, p.n_seqs, p.chunk, cid, b, c);
+        if (b < 0) break;
+      }
       const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
       const int key0 = c * p.chunk;
-      const int nk = min(p.chunk, L - key0);
+      int nk;
+      if constexpr (MODE == DEC_SELECTED)
+        nk = dec_selected_keys(p, b, (hb * p.RB) / p.R, key0);
+      else
+        nk = min(p.chunk, L - key0);
       const int n_tiles = (nk + C::BK - 1) / C::BK;
       const int pos = L - 1;  // the query is the newest token of its request
       // q fragments: rows g8 and g8+8 are heads hb*RB + row (zero when row >= RB).
@@ -320,8 +379,31 @@ __global__ void __launch_bounds__(160, 1)
       float o[D / 8][4];
 #pragma unroll
       for (int n = 0; n < D / 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+      // DEC_SELECTED: the list entry of this warp's 16 keys of a tile (one block, since block
+      // sizes are multiples of 16), read a tile ahead.
+      auto entry = [&](int t) {
+        const int j = (key0 + t * C::BK + warp * 16) / p.block_size;
+        return (t < n_tiles && j < p.n_select)
+                   ? __ldg(p.selected +
+                           (static_cast<size_t>(b) * (p.hq / p.R) + (hb * p.RB) / p.R) *
+                               p.n_select + j)
+                   : -1;
+      };
+      int e_next = MODE == DEC_SELECTED ? entry(0) : 0;
 
       for (int t = 0; t < n_tiles; ++t) {
+        // Key index, in the request, of this warp's first key of the tile, and how many of its 16
+        // keys exist.
+        int first = key0 + t * C::BK + warp * 16;
+        int live = 16;
+        if constexpr (MODE == DEC_SELECTED) {
+          const int e = e_next;
+          e_next = entry(t + 1);
+          // (an entry past the request's blocks names no key; its product must not wrap)
+          const bool in = e >= 0 && e < (L + p.block_size - 1) / p.block_size;
+          first = in ? e * p.block_size + first % p.block_size : 0;
+          live = in ? L - first : 0;
+        }
         const uint32_t s = cnt % C::NS;
         const uint32_t ph = (cnt / C::NS) & 1u;
         ok = mbar_wait(DBAR(B_F + s), ph, abort_flag, tmo, ecode | 2);
@@ -330,7 +412,19 @@ __global__ void __launch_bounds__(160, 1)
         const uint32_t kst = sbase + C::SMEM_RING + s * C::STAGE_BYTES;
         const uint32_t vst = kst + C::KT_BYTES;
         bool zeroed = false;
-        if constexpr (PAGED) {
+        if constexpr (MODE == DEC_SELECTED) {
+          // The same for a listed block that the sequence ends in, wherever it stands in the
+          // list (a slot past the end may hold anything).
+          if (live < 16) {
+            const int r0 = max(live, 0);
+            for (int i = lane; i < (16 - r0) * (D / 8); i += 32) {
+              const int rr = warp * 16 + r0 + i / (D / 8), ch = i % (D / 8);
+              st_shared_v4(dec_row_addr<D>(vst, rr, ch ^ (rr & 7), p.lay_log2), 0, 0, 0, 0);
+            }
+            zeroed = true;
+            __syncwarp();
+          }
+        } else if constexpr (PAGED) {
           // A cache block's slots past the sequence end may hold anything (0 * NaN is NaN in
           // P V): zero this warp's V rows past the last key of a partial tile.
           const int valid = nk - t * C::BK;
@@ -364,7 +458,7 @@ __global__ void __launch_bounds__(160, 1)
           }
         }
         // ---- online softmax over the 16 keys (rows g8 / g8+8)
-        const int kbase = key0 + t * C::BK + warp * 16;  // key index (in request) of col 0
+        const int kbase = first;  // key index (in request) of col 0
         float x[2][4];
         float mx_lo = -INFINITY, mx_hi = -INFINITY;
 #pragma unroll
@@ -372,7 +466,8 @@ __global__ void __launch_bounds__(160, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int key = kbase + n * 8 + 2 * t4 + e;
-            const bool kv = key < key0 + nk;
+            const bool kv =
+                MODE == DEC_SELECTED ? n * 8 + 2 * t4 + e < live : key < key0 + nk;
             float a = sc[n][e] * p.c1, bb = sc[n][2 + e] * p.c1;
             if constexpr (ALIBI) {
               const float dist = static_cast<float>(pos - key);
@@ -383,6 +478,18 @@ __global__ void __launch_bounds__(160, 1)
             x[n][2 + e] = kv ? bb : -INFINITY;
             mx_lo = fmaxf(mx_lo, x[n][e]);
             mx_hi = fmaxf(mx_hi, x[n][2 + e]);
+          }
+        }
+        if constexpr (MODE == DEC_WEIGHTS) {
+          // Scores of existing heads and of the whole chunk's range: 32 bytes per row and n-tile.
+          const int kc = t * C::BK + warp * 16 + 2 * t4;  // key in the chunk
+          float* sl = p.ws_s + (static_cast<size_t>(cid) * p.hq + h_lo) * p.chunk + kc;
+#pragma unroll
+          for (int n = 0; n < 2; ++n) {
+            if (v_lo) *reinterpret_cast<float2*>(sl + n * 8) = make_float2(x[n][0], x[n][1]);
+            if (v_hi)
+              *reinterpret_cast<float2*>(sl + static_cast<size_t>(8) * p.chunk + n * 8) =
+                  make_float2(x[n][2], x[n][3]);
           }
         }
 #pragma unroll
@@ -490,6 +597,19 @@ __global__ void __launch_bounds__(160, 1)
           const int head = hb * p.RB + row;
           const size_t slot = static_cast<size_t>(cid) * p.hq + head;
           const int d = pass * C::MC + dc;
+          if constexpr (MODE == DEC_SELECTED) {
+            // One chunk per request: this partial is the result (no merge is launched).
+            if (p.n_chunks == 1) {
+              using OutT = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+              if (d < p.dh)
+                reinterpret_cast<OutT*>(p.out)[slot * p.dh + d] =
+                    static_cast<OutT>(Lsum > 0.f ? acc / Lsum : 0.f);
+              if (d == 0 && p.lse)
+                p.lse[static_cast<size_t>(head) * p.n_seqs + b] =
+                    Lsum > 0.f ? (M + __log2f(Lsum)) * LN2 : -INFINITY;
+              continue;
+            }
+          }
           p.ws_o[slot * D + d] = Lsum > 0.f ? acc / Lsum : 0.f;
           if (d == 0) p.ws_lse[slot] = Lsum > 0.f ? (M + __log2f(Lsum)) * LN2 : -INFINITY;
         }
@@ -508,7 +628,8 @@ __global__ void __launch_bounds__(160, 1)
 
 // Merge kernel: one CTA per (request, KV group); lse = ln sum_c exp(lse_c),
 // out = sum_c exp(lse_c - lse) O_c, cast to the output dtype.
-template <int D, bool BF16>
+// FIXED: every request has p.n_chunks chunks (DEC_SELECTED); otherwise its length gives them.
+template <int D, bool BF16, bool FIXED = false>
 __global__ void __launch_bounds__(256)
     mea_lse_merge_kernel(const DecParams p) {
   // One CTA per (request b, KV group g): the R heads of the group, all their chunk partials.
@@ -520,9 +641,9 @@ __global__ void __launch_bounds__(256)
   __shared__ int s_start;
   __shared__ float s_m[64], s_z[64];
   const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
-  const int n = (L + p.chunk - 1) / p.chunk;
+  const int n = FIXED ? p.n_chunks : (L + p.chunk - 1) / p.chunk;
   if (threadIdx.x < 32) {
-    const int st = dec_chunk_start(p.cu_k, b, p.chunk);
+    const int st = FIXED ? b * p.n_chunks : dec_chunk_start(p.cu_k, b, p.chunk);
     if (threadIdx.x == 0) s_start = st;
   }
   __syncthreads();
@@ -581,6 +702,75 @@ __global__ void __launch_bounds__(256)
         p.lse[static_cast<size_t>(head) * p.n_seqs + b] = z > 0.f ? m + __logf(z) : -INFINITY;
     }
     __syncthreads();
+  }
+}
+
+// Attention weights of a decode step: thread t of CTA (key range, KV head g, request b) takes one
+// key and adds exp2(score - lse) over the R heads of the group, in head order, to the key's
+// previous weight. The row's lse comes from its chunks' lse, as in the merge above.
+// Bound by memory: it reads the scores that the split kernel wrote (4 R bytes a key, part of
+// them still in L2) and reads and writes 4 bytes of weight a key.
+template <int R_MAX>
+__global__ void __launch_bounds__(256)
+    mea_decode_weights_kernel(const DecParams p) {
+  constexpr float LOG2E = 1.4426950408889634f;
+  const int b = blockIdx.z, g = blockIdx.y;
+  int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
+  if (p.w_stride < L) L = static_cast<int>(p.w_stride);  // never past the row of weights
+  const int t0 = blockIdx.x * 1024;
+  if (t0 >= L) return;
+  __shared__ int s_start;
+  __shared__ float s_lse[R_MAX];
+  const int n = dec_nchunks(p.cu_k, b, p.chunk);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int st = dec_chunk_start(p.cu_k, b, p.chunk);
+  if (threadIdx.x == 0) s_start = st;
+  const float* prev = p.prev ? p.prev + (static_cast<size_t>(b) * gridDim.y + g) * p.w_stride
+                             : nullptr;
+  float* out = p.weights + (static_cast<size_t>(b) * gridDim.y + g) * p.w_stride;
+  float w[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int t = t0 + u * 256 + threadIdx.x;
+    w[u] = (prev && t < L) ? prev[t] : 0.f;
+  }
+  for (int rb = 0; rb < p.R; rb += R_MAX) {  // heads of the group, R_MAX at a time
+    const int rn = min(R_MAX, p.R - rb);
+    for (int rr = warp; rr < rn; rr += 8) {
+      const int head = g * p.R + rb + rr;
+      float m = -INFINITY, z = 0.f;
+      for (int c = lane; c < n; c += 32)
+        m = fmaxf(m, p.ws_lse[static_cast<size_t>(st + c) * p.hq + head]);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+      if (m != -INFINITY)
+        for (int c = lane; c < n; c += 32)
+          z += __expf(p.ws_lse[static_cast<size_t>(st + c) * p.hq + head] - m);
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) z += __shfl_xor_sync(0xffffffffu, z, off);
+      // (log2 units; +inf where the row attends to nothing, so that its weights are 0)
+      if (lane == 0) s_lse[rr] = z > 0.f ? (m + __logf(z)) * LOG2E : INFINITY;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int t = t0 + u * 256 + threadIdx.x;
+      if (t < L) {
+        const int c = t / p.chunk;
+        const float* sc = p.ws_s +
+                          (static_cast<size_t>(s_start + c) * p.hq + g * p.R + rb) * p.chunk +
+                          (t - c * p.chunk);
+#pragma unroll 8
+        for (int rr = 0; rr < rn; ++rr)
+          w[u] += ex2_approx(__ldcs(sc + static_cast<size_t>(rr) * p.chunk) - s_lse[rr]);
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int t = t0 + u * 256 + threadIdx.x;
+    if (t < L) out[t] = w[u];
   }
 }
 

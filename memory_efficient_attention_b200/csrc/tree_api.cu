@@ -1,0 +1,233 @@
+// tree_api.cu — C ABI of the tree attention over a paged cache and of a prompt's attention weights
+// (declared in include/mea.h): argument checks, TMA descriptors and launches. No device memory is
+// allocated and no call synchronises the host.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "../../include/mea.h"
+#include "host_util.h"
+#include "tree_sm100.cuh"
+#include "weights_sm100.cuh"
+
+using namespace mea_host;
+
+namespace mea_tree {
+// This translation unit's device error word (see mea_device_error).
+__attribute__((visibility("hidden"))) int device_error(unsigned int* code, bool clear) {
+  if (cudaMemcpyFromSymbol(code, mea::g_mea_error, sizeof(*code)) != cudaSuccess)
+    return MEA_ERR_CUDA;
+  const unsigned int z = 0;
+  if (clear && cudaMemcpyToSymbol(mea::g_mea_error, &z, sizeof(z)) != cudaSuccess)
+    return MEA_ERR_CUDA;
+  return MEA_OK;
+}
+}  // namespace mea_tree
+
+namespace {
+
+template <int D, bool BF16, bool ALIBI>
+int launch_tree(const CUtensorMap& tk, const CUtensorMap& tv, const mea::TreeParams& p, int grid,
+                cudaStream_t s) {
+  constexpr auto kern = mea::mea_tree_sm100_kernel<D, BF16, ALIBI>;
+  using C = mea::TreeCfg<D>;
+  if (smem_attr_once<kern>(C::SMEM_TOTAL) != cudaSuccess) return MEA_ERR_CUDA;
+  clear_stale_launch_error();
+  kern<<<grid, C::THREADS, C::SMEM_TOTAL, s>>>(tk, tv, p);
+  if (grid > 1)
+    mea::mea_tree_merge_kernel<D, BF16>
+        <<<dim3(static_cast<unsigned>(grid - 1), C::ROWS / 8), 256, 0, s>>>(p, grid);
+  return cudaGetLastError() == cudaSuccess ? MEA_OK : MEA_ERR_CUDA;
+}
+
+template <int D, bool BF16, bool CAUSAL, bool ALIBI>
+int launch_weights(const CUtensorMap& tq, const CUtensorMap& tk, const mea::WeightsParams& p,
+                   dim3 grid, cudaStream_t s) {
+  constexpr auto kern = mea::mea_weights_sm100_kernel<D, BF16, CAUSAL, ALIBI>;
+  using C = mea::WeightsCfg<D>;
+  if (smem_attr_once<kern>(C::SMEM_TOTAL) != cudaSuccess) return MEA_ERR_CUDA;
+  clear_stale_launch_error();
+  kern<<<grid, C::THREADS, C::SMEM_TOTAL, s>>>(tq, tk, p);
+  return cudaGetLastError() == cudaSuccess ? MEA_OK : MEA_ERR_CUDA;
+}
+
+template <int D, bool BF16>
+int launch_weights_d(bool causal, const CUtensorMap& tq, const CUtensorMap& tk,
+                     const mea::WeightsParams& p, dim3 grid, cudaStream_t s) {
+  const bool al = p.slopes != nullptr;
+  if (causal)
+    return al ? launch_weights<D, BF16, true, true>(tq, tk, p, grid, s)
+              : launch_weights<D, BF16, true, false>(tq, tk, p, grid, s);
+  return al ? launch_weights<D, BF16, false, true>(tq, tk, p, grid, s)
+            : launch_weights<D, BF16, false, false>(tq, tk, p, grid, s);
+}
+
+size_t tree_rows(int d) { return d > 128 ? mea::TreeCfg<256>::ROWS : mea::TreeCfg<128>::ROWS; }
+// Two partial ranges per CTA: ROWS rows of the kernel's width, then ROWS log-sum-exps, in fp32.
+size_t tree_ws_lse(int d, int sms) {
+  return 2 * static_cast<size_t>(sms) * tree_rows(d) * padded_head_dim(d) * sizeof(float);
+}
+size_t tree_ws(int d, int sms) {
+  return tree_ws_lse(d, sms) + 2 * static_cast<size_t>(sms) * tree_rows(d) * sizeof(float);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t mea_decode_tree_workspace_size(int n_heads_q, int n_heads_kv, int head_dim) {
+  if (n_heads_q < 1 || n_heads_kv < 1 || n_heads_q % n_heads_kv || !dec_head_dim_ok(head_dim))
+    return 0;
+  DeviceInfo di;
+  return tree_ws(head_dim, current_device_info(di) == MEA_OK ? di.sms : 148);
+}
+
+int mea_decode_tree(const void* q, const void* k_cache, const void* v_cache,
+                    const int32_t* block_table, const int32_t* cu_seqlens_q,
+                    const int32_t* cu_seqlens_k, const int32_t* tree_mask, void* out, float* lse,
+                    int n_seqs, int total_q, int max_seqlen_q, int max_seqlen_k, int mask_words,
+                    int num_blocks, int block_size, int max_blocks, int n_heads_q,
+                    int n_heads_kv, int head_dim, float scale, const float* alibi_slopes,
+                    int dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!q || !k_cache || !v_cache || !block_table || !cu_seqlens_q || !cu_seqlens_k ||
+      !tree_mask || !out)
+    return MEA_ERR_NULL;
+  if (n_seqs < 1 || total_q < 0 || max_seqlen_q < 0 || max_seqlen_q > total_q ||
+      max_seqlen_k < 0 || mask_words < 1 ||
+      static_cast<long long>(mask_words) * 32 < max_seqlen_q || num_blocks < 1 ||
+      max_blocks < 1 || static_cast<long long>(max_blocks) * block_size < max_seqlen_k)
+    return MEA_ERR_SHAPE;
+  if (!(block_size == 16 || block_size == 32 || (block_size >= 64 && block_size % 64 == 0)))
+    return MEA_ERR_SHAPE;
+  if (n_heads_q < 1 || n_heads_kv < 1 || n_heads_q % n_heads_kv != 0) return MEA_ERR_HEADS;
+  if (static_cast<long long>(total_q) * (n_heads_q / n_heads_kv) > 0x3fffffffll)
+    return MEA_ERR_SHAPE;
+  if (!dec_head_dim_ok(head_dim)) return MEA_ERR_HEAD_DIM;
+  if (dtype != MEA_F16 && dtype != MEA_BF16) return MEA_ERR_DTYPE;
+  if (!std::isfinite(scale)) return MEA_ERR_SCALE;
+  if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+      (lse && !aligned(lse, 4)) || !aligned(cu_seqlens_q, 4) || !aligned(cu_seqlens_k, 4) ||
+      !aligned(block_table, 4) || !aligned(tree_mask, 4) ||
+      (alibi_slopes && !aligned(alibi_slopes, 4)))
+    return MEA_ERR_ALIGN;
+  if (!workspace || !aligned(workspace, 256)) return MEA_ERR_WORKSPACE;
+  DeviceInfo di;
+  if (int rc = current_device_info(di); rc != MEA_OK) return rc;
+  if (workspace_bytes < tree_ws(head_dim, di.sms)) return MEA_ERR_WORKSPACE;
+  if (total_q == 0 || max_seqlen_q == 0) return MEA_OK;
+
+  mea::TreeParams p{};
+  p.q = q;
+  p.out = out;
+  p.lse = lse;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.block_table = block_table;
+  p.mask = reinterpret_cast<const uint32_t*>(tree_mask);
+  p.slopes = alibi_slopes;
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_lse =
+      reinterpret_cast<float*>(static_cast<char*>(workspace) + tree_ws_lse(head_dim, di.sms));
+  p.n_seqs = n_seqs;
+  p.total_q = total_q;
+  p.hq = n_heads_q;
+  p.hkv = n_heads_kv;
+  p.dh = head_dim;
+  p.R = n_heads_q / n_heads_kv;
+  p.mask_words = mask_words;
+  p.block_size = block_size;
+  p.max_blocks = max_blocks;
+  p.num_blocks = num_blocks;
+  p.box_rows = block_size < 64 ? block_size : 64;
+  p.c1 = scale * 1.4426950408889634f;
+  p.timeout_ns = g_timeout_ns.load();
+  CUtensorMap tk, tv;
+  if (!encode_4d(&tk, k_cache, dtype, head_dim, n_heads_kv, block_size, num_blocks, 64, 1,
+                 p.box_rows, 1) ||
+      !encode_4d(&tv, v_cache, dtype, head_dim, n_heads_kv, block_size, num_blocks, 64, 1,
+                 p.box_rows, 1))
+    return MEA_ERR_CUDA;
+  // No more CTAs than tiles.
+  const long long rows = static_cast<long long>(tree_rows(head_dim));
+  const long long parts = (static_cast<long long>(max_seqlen_q) * p.R + rows - 1) / rows;
+  const long long tiles = max_seqlen_k > 128 ? (static_cast<long long>(max_seqlen_k) + 127) / 128
+                                             : 1;
+  const double bound = static_cast<double>(n_seqs) * n_heads_kv * parts * tiles;
+  const int grid = bound < di.sms ? static_cast<int>(bound) : di.sms;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool bf = dtype == MEA_BF16, al = alibi_slopes != nullptr;
+#define MEA_TREE(DD)                                                                        \
+  return bf ? (al ? launch_tree<DD, true, true>(tk, tv, p, grid, s)                         \
+                  : launch_tree<DD, true, false>(tk, tv, p, grid, s))                       \
+            : (al ? launch_tree<DD, false, true>(tk, tv, p, grid, s)                        \
+                  : launch_tree<DD, false, false>(tk, tv, p, grid, s))
+  if (head_dim > 128) MEA_TREE(256);
+  if (head_dim > 64) MEA_TREE(128);
+  MEA_TREE(64);
+#undef MEA_TREE
+}
+
+int mea_attention_weights(const void* q, const void* k, const float* lse,
+                          const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
+                          float* weights, long long weights_stride, int n_seqs, int total_q,
+                          int total_k, int max_seqlen_q, int max_seqlen_k, int n_heads_q,
+                          int n_heads_kv, int head_dim, float scale, int mask_kind,
+                          const float* alibi_slopes, int last_queries, int dtype, void* stream) {
+  if (!q || !k || !lse || !cu_seqlens_q || !cu_seqlens_k || !weights) return MEA_ERR_NULL;
+  if (n_seqs < 1 || total_q < 0 || total_k < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 ||
+      max_seqlen_q > total_q || max_seqlen_k > total_k || weights_stride < max_seqlen_k ||
+      last_queries < 0)
+    return MEA_ERR_SHAPE;
+  if (n_heads_q < 1 || n_heads_kv < 1 || n_heads_q % n_heads_kv != 0) return MEA_ERR_HEADS;
+  const long long tiles = (static_cast<long long>(max_seqlen_k) + 127) / 128;
+  if (tiles > 65535 || static_cast<long long>(n_seqs) * n_heads_kv > 0x7fffffffll)
+    return MEA_ERR_SHAPE;
+  if (!dec_head_dim_ok(head_dim)) return MEA_ERR_HEAD_DIM;
+  if (dtype != MEA_F16 && dtype != MEA_BF16) return MEA_ERR_DTYPE;
+  if (mask_kind != MEA_MASK_NONE && mask_kind != MEA_MASK_CAUSAL) return MEA_ERR_MASK;
+  if (!std::isfinite(scale)) return MEA_ERR_SCALE;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(lse, 4) || !aligned(cu_seqlens_q, 4) ||
+      !aligned(cu_seqlens_k, 4) || !aligned(weights, 4) ||
+      (alibi_slopes && !aligned(alibi_slopes, 4)))
+    return MEA_ERR_ALIGN;
+  DeviceInfo di;
+  if (int rc = current_device_info(di); rc != MEA_OK) return rc;
+  if (max_seqlen_k == 0) return MEA_OK;
+  mea::WeightsParams p{};
+  p.lse = lse;
+  p.cu_q = cu_seqlens_q;
+  p.cu_k = cu_seqlens_k;
+  p.slopes = alibi_slopes;
+  p.weights = weights;
+  p.w_stride = weights_stride;
+  p.n_seqs = n_seqs;
+  p.total_q = total_q;
+  p.hq = n_heads_q;
+  p.hkv = n_heads_kv;
+  p.R = n_heads_q / n_heads_kv;
+  p.last = last_queries;
+  p.c1 = scale * 1.4426950408889634f;
+  p.timeout_ns = g_timeout_ns.load();
+  CUtensorMap tq, tk;
+  const uint64_t q_rows = total_q > 0 ? static_cast<uint64_t>(total_q) : 1;
+  if (!encode_3d(&tq, q, dtype, head_dim, n_heads_q, q_rows, 64, 1, 128) ||
+      !encode_3d(&tk, k, dtype, head_dim, n_heads_kv, total_k, 64, 1, 128))
+    return MEA_ERR_CUDA;
+  // Key tile 0 first: under a causal mask it has the most queries.
+  const dim3 grid(static_cast<unsigned>(n_seqs) * static_cast<unsigned>(n_heads_kv),
+                  static_cast<unsigned>(tiles));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool causal = mask_kind == MEA_MASK_CAUSAL, bf = dtype == MEA_BF16;
+  if (head_dim > 128)
+    return bf ? launch_weights_d<256, true>(causal, tq, tk, p, grid, s)
+              : launch_weights_d<256, false>(causal, tq, tk, p, grid, s);
+  if (head_dim > 64)
+    return bf ? launch_weights_d<128, true>(causal, tq, tk, p, grid, s)
+              : launch_weights_d<128, false>(causal, tq, tk, p, grid, s);
+  return bf ? launch_weights_d<64, true>(causal, tq, tk, p, grid, s)
+            : launch_weights_d<64, false>(causal, tq, tk, p, grid, s);
+}
+
+}  // extern "C"
