@@ -399,71 +399,131 @@ def decode_splitkv_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
 # ------------------------------------------------------------------------------------------
 # Operators on a paged K/V cache beside the plain decode.
 # ------------------------------------------------------------------------------------------
+# These checks run before every decode step's launches, whose kernels can be as short as the checks:
+# they compare device indices and shapes directly and copy nothing that fits already.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_cur_device = torch._C._cuda_getDevice
+_INV_SQRT: dict = {}  # head dim -> 1 / sqrt
+
+
+def _gpu_index(t: torch.Tensor) -> int:
+    i = t.get_device()
+    if i < 0:
+        raise MeaError(_lib.MEA_ERR_DEVICE, "tensors must live on the GPU")
+    return i
+
+
+def _same_gpu(name: str, t: torch.Tensor, idx: int) -> None:
+    if t.get_device() != idx:
+        raise MeaError(_lib.MEA_ERR_DEVICE, f"{name} must be a CUDA tensor on cuda:{idx}")
+
+
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _check_prefix(name: str, t: torch.Tensor, n: int, idx: int) -> torch.Tensor:
+    """An int32 ``[n]`` tensor on GPU ``idx`` (made contiguous)."""
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n:
+        raise MeaError(_lib.MEA_ERR_SHAPE, f"{name} must be int32 [{n}]")
+    _same_gpu(name, t, idx)
+    return _dense(t)
+
+
 def _check_paged(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor],
                  block_table: torch.Tensor, cu_seqlens_k: torch.Tensor,
                  q: Optional[torch.Tensor] = None):
     """A cache ``[num_blocks, block_size, Hkv, D]`` with its block table and key counts: contiguous,
     on one GPU, and, with ``q [rows, Hq, D]``, of its dtype and head dim. (A cache is never copied
-    here to make it contiguous.) Returns the block table and the prefix sums, contiguous."""
-    dev = k_cache.device
-    if not k_cache.is_cuda:
-        raise MeaError(_lib.MEA_ERR_DEVICE, "tensors must live on the GPU")
-    if k_cache.dim() != 4 or not k_cache.is_contiguous() or (
-            v_cache is not None and (v_cache.shape != k_cache.shape
-                                     or not v_cache.is_contiguous())):
+    here to make it contiguous.) Returns the GPU's index, the cache's shape and dtype code, the
+    block table and the prefix sums (contiguous)."""
+    idx = _gpu_index(k_cache)
+    shape = k_cache.shape
+    if len(shape) != 4 or not k_cache.is_contiguous():
         raise MeaError(_lib.MEA_ERR_SHAPE,
                        "caches must be contiguous [num_blocks, block_size, Hkv, D] tensors")
-    if v_cache is not None and (v_cache.dtype != k_cache.dtype or v_cache.device != dev):
-        raise MeaError(_lib.MEA_ERR_DTYPE, "k_cache and v_cache must share one dtype and GPU")
+    dtype = k_cache.dtype
+    if v_cache is not None:
+        if v_cache.shape != shape or not v_cache.is_contiguous():
+            raise MeaError(_lib.MEA_ERR_SHAPE, "k_cache and v_cache must be alike and contiguous")
+        if v_cache.dtype is not dtype:
+            raise MeaError(_lib.MEA_ERR_DTYPE, "k_cache and v_cache must share one dtype")
+        _same_gpu("v_cache", v_cache, idx)
     if q is not None:
-        if q.dim() != 3 or q.shape[2] != k_cache.shape[3]:
+        if q.dim() != 3 or q.size(2) != shape[3]:
             raise MeaError(_lib.MEA_ERR_SHAPE, "q must be [rows, Hq, D] with the cache's D")
-        if q.dtype != k_cache.dtype:
+        if q.dtype is not dtype:
             raise MeaError(_lib.MEA_ERR_DTYPE, "q and the cache must share one dtype")
-        if q.device != dev:
-            raise MeaError(_lib.MEA_ERR_DEVICE, f"q must be a CUDA tensor on {dev}")
-    if block_table.dim() != 2 or block_table.dtype != torch.int32:
+        _same_gpu("q", q, idx)
+    if block_table.dim() != 2 or block_table.dtype is not torch.int32:
         raise MeaError(_lib.MEA_ERR_SHAPE, "block_table must be int32 [n_seqs, max_blocks]")
-    _on_device(dev, block_table=block_table)
-    cu = _check_cu("cu_seqlens_k", cu_seqlens_k, block_table.shape[0] + 1, dev)
-    return block_table.contiguous(), cu
+    _same_gpu("block_table", block_table, idx)
+    cu = _check_prefix("cu_seqlens_k", cu_seqlens_k, block_table.size(0) + 1, idx)
+    return idx, shape, _dtype_code(dtype), _dense(block_table), cu
 
 
-def _launch(device: torch.device, name: str, *args) -> None:
-    """Calls library function ``name`` with ``device`` current and its current stream as the last
-    argument (a launch goes to the current device, whichever the tensors live on)."""
-    fn = getattr(_lib.load(), name)
-    if torch.cuda.current_device() == device.index:
-        rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            rc = fn(*args, torch.cuda.current_stream(device).cuda_stream)
-    if rc != _lib.MEA_OK:
-        raise MeaError(rc, name)
-
-
-def _slopes_for(alibi_slopes: Optional[torch.Tensor], hq: int, device: torch.device):
+def _slopes_for(alibi_slopes: Optional[torch.Tensor], hq: int, idx: int):
     if alibi_slopes is None:
         return None
-    if tuple(alibi_slopes.shape) != (hq,):
+    if alibi_slopes.dim() != 1 or alibi_slopes.numel() != hq:
         raise MeaError(_lib.MEA_ERR_SHAPE, f"alibi_slopes must be [{hq}]")
-    return alibi_slopes.to(device=device, dtype=torch.float32).contiguous()
+    if alibi_slopes.dtype is not torch.float32 or alibi_slopes.get_device() != idx:
+        alibi_slopes = alibi_slopes.to(device=f"cuda:{idx}", dtype=torch.float32)
+    return _dense(alibi_slopes)
 
 
-def _output(name, t, shape, dtype, device) -> torch.Tensor:
+def _scale_for(scale: Optional[float], d: int) -> float:
+    if scale is not None:
+        return float(scale)
+    inv = _INV_SQRT.get(d)
+    if inv is None:
+        inv = _INV_SQRT[d] = 1.0 / math.sqrt(d) if d > 0 else 0.0
+    return inv
+
+
+def _output(name, t, shape, dtype, idx: int) -> torch.Tensor:
+    """An output: made here, or the caller's, which must match exactly."""
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    return _check_buffer(name, t, shape, dtype, device)
+        return torch.empty(shape, dtype=dtype, device=f"cuda:{idx}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != idx \
+            or not t.is_contiguous():
+        raise MeaError(_lib.MEA_ERR_SHAPE,
+                       f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                       f"on cuda:{idx}")
+    return t
 
 
-def _check_weights(name: str, t: torch.Tensor, n: int, hkv: int, max_k: int,
-                   device: torch.device) -> torch.Tensor:
-    if t.dim() != 3 or t.shape[0] != n or t.shape[1] != hkv or t.shape[2] < max_k \
-            or t.dtype != torch.float32 or t.device != device or not t.is_contiguous():
+def _scratch(t: Optional[torch.Tensor], size, idx: int):
+    """The workspace (made here, of ``size()`` bytes, when the caller gives none) and its bytes."""
+    if t is None:
+        t = torch.empty(size(), dtype=torch.uint8, device=f"cuda:{idx}")
+    elif t.get_device() != idx or not t.is_contiguous():
+        raise MeaError(_lib.MEA_ERR_WORKSPACE, f"workspace must be contiguous on cuda:{idx}")
+    return t, t.numel() * t.element_size()
+
+
+def _check_weights(name: str, t: torch.Tensor, n: int, hkv: int, max_k: int, idx: int) -> int:
+    """fp32 ``[n, hkv, >= max_k]``; returns its row length."""
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != n or shape[1] != hkv or shape[2] < max_k \
+            or t.dtype is not torch.float32 or t.get_device() != idx or not t.is_contiguous():
         raise MeaError(_lib.MEA_ERR_SHAPE,
                        f"{name} must be a contiguous float32 [{n}, {hkv}, >= {max_k}] tensor on "
-                       f"{device}")
-    return t
+                       f"cuda:{idx}")
+    return shape[2]
+
+
+def _launch(idx: int, name: str, *args) -> None:
+    """Calls library function ``name`` with GPU ``idx`` current and its current stream as the last
+    argument (a launch goes to the current device, whichever the tensors live on)."""
+    fn = getattr(_lib.load(), name)
+    if _cur_device() == idx:
+        rc = fn(*args, _raw_stream(idx))
+    else:
+        with torch.cuda.device(idx):
+            rc = fn(*args, _raw_stream(idx))
+    if rc != _lib.MEA_OK:
+        raise MeaError(rc, name)
 
 
 def block_key_bounds(k_cache: torch.Tensor, block_table: torch.Tensor,
@@ -475,20 +535,18 @@ def block_key_bounds(k_cache: torch.Tensor, block_table: torch.Tensor,
     :func:`select_blocks` reads. With ``first_key`` (int32 ``[n_seqs]``) only the blocks that hold a
     request's keys from ``first_key[b]`` on are done: after a decode step, its newest key's block.
     Blocks in no request's table are left as they were (zeros when ``bounds`` is made here)."""
-    table, cu = _check_paged(k_cache, None, block_table, cu_seqlens_k)
-    nb, bs, hkv, d = k_cache.shape
-    dev = k_cache.device
-    n = table.shape[0]
+    idx, (nb, bs, hkv, d), code, table, cu = _check_paged(k_cache, None, block_table,
+                                                          cu_seqlens_k)
+    n, max_blocks = table.shape
+    first = None
     if first_key is not None:
-        first_key = _check_cu("first_key", first_key, n, dev)
+        first = _check_prefix("first_key", first_key, n, idx)
     if bounds is None:
-        bounds = torch.zeros((nb, hkv, 2, d), dtype=k_cache.dtype, device=dev)
+        bounds = torch.zeros((nb, hkv, 2, d), dtype=k_cache.dtype, device=k_cache.device)
     else:
-        _check_buffer("bounds", bounds, (nb, hkv, 2, d), k_cache.dtype, dev)
-    _launch(
-        dev, "mea_block_key_bounds",
-        _ptr(k_cache), _ptr(table), _ptr(cu), _ptr(first_key), _ptr(bounds), n, nb, bs,
-        table.shape[1], int(max_seqlen_k), hkv, d, _dtype_code(k_cache.dtype))
+        _output("bounds", bounds, (nb, hkv, 2, d), k_cache.dtype, idx)
+    _launch(idx, "mea_block_key_bounds", k_cache.data_ptr(), table.data_ptr(), cu.data_ptr(),
+            _ptr(first), bounds.data_ptr(), n, nb, bs, max_blocks, int(max_seqlen_k), hkv, d, code)
     return bounds
 
 
@@ -501,29 +559,29 @@ def select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tens
     the greatest sum over the group's heads of ``q . k``. Returns int32
     ``[n_seqs, Hkv, n_select]``, block indices within the request in ascending order, -1 after the
     last one when the request has fewer blocks. Equal scores: the lower index."""
-    if q.dim() != 3 or bounds.dim() != 4 or bounds.shape[2] != 2 \
-            or bounds.shape[3] != q.shape[2]:
+    idx = _gpu_index(q)
+    if q.dim() != 3 or bounds.dim() != 4 or bounds.size(2) != 2 or bounds.size(3) != q.size(2):
         raise MeaError(_lib.MEA_ERR_SHAPE, "q [n_seqs, Hq, D], bounds [num_blocks, Hkv, 2, D]")
-    if not q.is_cuda:
-        raise MeaError(_lib.MEA_ERR_DEVICE, "tensors must live on the GPU")
-    if q.dtype != bounds.dtype:
+    if q.dtype is not bounds.dtype:
         raise MeaError(_lib.MEA_ERR_DTYPE, "q and bounds must share one dtype")
-    dev = q.device
-    _on_device(dev, bounds=bounds, block_table=block_table)
+    _same_gpu("bounds", bounds, idx)
+    _same_gpu("block_table", block_table, idx)
     n, hq, d = q.shape
-    nb, hkv = bounds.shape[:2]
-    if block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.shape[0] != n:
+    nb, hkv = bounds.size(0), bounds.size(1)
+    if block_table.dtype is not torch.int32 or block_table.dim() != 2 or block_table.size(0) != n:
         raise MeaError(_lib.MEA_ERR_SHAPE, "block_table must be int32 [n_seqs, max_blocks]")
     if not bounds.is_contiguous():
         raise MeaError(_lib.MEA_ERR_SHAPE, "bounds must be contiguous")
-    q, block_table = q.contiguous(), block_table.contiguous()
-    cu = _check_cu("cu_seqlens_k", cu_seqlens_k, n + 1, dev)
-    selected = _output("selected", selected, (n, hkv, int(n_select)), torch.int32, dev)
-    _launch(
-        dev, "mea_select_blocks",
-        _ptr(q), _ptr(bounds), _ptr(block_table), _ptr(cu), _ptr(selected), n, nb, int(block_size),
-        block_table.shape[1], int(max_seqlen_k), hq, hkv, d, int(n_select), int(n_first),
-        int(n_last), _dtype_code(q.dtype))
+    n_select = int(n_select)
+    if n_select < 1:
+        raise MeaError(_lib.MEA_ERR_SHAPE, "n_select must be at least 1")
+    q, table = _dense(q), _dense(block_table)
+    cu = _check_prefix("cu_seqlens_k", cu_seqlens_k, n + 1, idx)
+    selected = _output("selected", selected, (n, hkv, n_select), torch.int32, idx)
+    _launch(idx, "mea_select_blocks", q.data_ptr(), bounds.data_ptr(), table.data_ptr(),
+            cu.data_ptr(), selected.data_ptr(), n, nb, int(block_size), table.size(1),
+            int(max_seqlen_k), hq, hkv, d, n_select, int(n_first), int(n_last),
+            _dtype_code(q.dtype))
     return selected
 
 
@@ -542,29 +600,25 @@ def decode_paged_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     """:func:`decode_paged` over the blocks in ``selected`` (:func:`select_blocks`) only. Entries may
     be in any order; one below 0 or past the request's blocks names no keys, a block listed twice
     counts twice. Returns ``(out [n_seqs, Hq, D], lse [Hq, n_seqs])``."""
-    table, cu = _check_paged(k_cache, v_cache, block_table, cu_seqlens_k, q)
-    q = q.contiguous()
-    n, hq, d = q.shape
-    nb, bs, hkv, _ = k_cache.shape
-    dev = q.device
-    if n != table.shape[0] or selected.dtype != torch.int32 or selected.dim() != 3 \
-            or tuple(selected.shape[:2]) != (n, hkv):
+    idx, (nb, bs, hkv, d), code, table, cu = _check_paged(k_cache, v_cache, block_table,
+                                                          cu_seqlens_k, q)
+    q = _dense(q)
+    n, hq, _ = q.shape
+    if n != table.size(0) or selected.dtype is not torch.int32 or selected.dim() != 3 \
+            or selected.size(0) != n or selected.size(1) != hkv:
         raise MeaError(_lib.MEA_ERR_SHAPE, f"selected must be int32 [{n}, {hkv}, n_select]")
-    _on_device(dev, selected=selected)
-    selected = selected.contiguous()
-    sel = selected.shape[2]
-    if workspace is None:
-        workspace = torch.empty(decode_selected_workspace_size(n, sel, bs, hq, hkv, d, split_keys),
-                                dtype=torch.uint8, device=dev)
-    out = _output("out", out, (n, hq, d), q.dtype, dev)
-    lse = _output("lse", lse, (hq, n), torch.float32, dev)
-    slopes = _slopes_for(alibi_slopes, hq, dev)
-    _launch(
-        dev, "mea_decode_selected",
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(cu), _ptr(selected), _ptr(out),
-        _ptr(lse), n, nb, bs, table.shape[1], sel, hq, hkv, d, 1.0 / math.sqrt(d) if scale is None
-        else float(scale), _ptr(slopes), _dtype_code(q.dtype), _ptr(workspace),
-        _check_workspace(workspace, dev), int(split_keys))
+    _same_gpu("selected", selected, idx)
+    selected = _dense(selected)
+    n_select = selected.size(2)
+    ws, ws_bytes = _scratch(workspace, lambda: decode_selected_workspace_size(
+        n, n_select, bs, hq, hkv, d, split_keys), idx)
+    out = _output("out", out, (n, hq, d), q.dtype, idx)
+    lse = _output("lse", lse, (hq, n), torch.float32, idx)
+    slopes = _slopes_for(alibi_slopes, hq, idx)
+    _launch(idx, "mea_decode_selected", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            table.data_ptr(), cu.data_ptr(), selected.data_ptr(), out.data_ptr(), lse.data_ptr(),
+            n, nb, bs, table.size(1), n_select, hq, hkv, d, _scale_for(scale, d), _ptr(slopes),
+            code, ws.data_ptr(), ws_bytes, int(split_keys))
     return out, lse
 
 
@@ -585,30 +639,26 @@ def decode_paged_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     its KV group and added to ``prev_weights`` (None: zeros; ``weights`` itself: accumulate in
     place), to ``weights`` fp32 ``[n_seqs, Hkv, >= max_seqlen_k]``; entries past a request's keys
     are left as they were. Returns ``(out [n_seqs, Hq, D], lse [Hq, n_seqs], weights)``."""
-    table, cu = _check_paged(k_cache, v_cache, block_table, cu_seqlens_k, q)
-    q = q.contiguous()
-    n, hq, d = q.shape
-    nb, bs, hkv, _ = k_cache.shape
-    dev = q.device
-    if n != table.shape[0]:
+    idx, (nb, bs, hkv, d), code, table, cu = _check_paged(k_cache, v_cache, block_table,
+                                                          cu_seqlens_k, q)
+    q = _dense(q)
+    n, hq, _ = q.shape
+    if n != table.size(0):
         raise MeaError(_lib.MEA_ERR_SHAPE, "block_table must have a row per request")
-    _check_weights("weights", weights, n, hkv, int(max_seqlen_k), dev)
+    max_k = int(max_seqlen_k)
+    width = _check_weights("weights", weights, n, hkv, max_k, idx)
     if prev_weights is not None:
-        _check_buffer("prev_weights", prev_weights, weights.shape, torch.float32, dev)
+        _output("prev_weights", prev_weights, weights.shape, torch.float32, idx)
     total = int(total_k_bound) if total_k_bound is not None else nb * bs
-    if workspace is None:
-        workspace = torch.empty(decode_weights_workspace_size(n, total, hq, hkv, d, split_keys),
-                                dtype=torch.uint8, device=dev)
-    out = _output("out", out, (n, hq, d), q.dtype, dev)
-    lse = _output("lse", lse, (hq, n), torch.float32, dev)
-    slopes = _slopes_for(alibi_slopes, hq, dev)
-    _launch(
-        dev, "mea_decode_weights",
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(cu), _ptr(out), _ptr(lse),
-        _ptr(weights), _ptr(prev_weights), weights.shape[2], n, nb, bs, table.shape[1], total,
-        int(max_seqlen_k), hq, hkv, d, 1.0 / math.sqrt(d) if scale is None else float(scale),
-        _ptr(slopes), _dtype_code(q.dtype), _ptr(workspace), _check_workspace(workspace, dev),
-        int(split_keys))
+    ws, ws_bytes = _scratch(workspace, lambda: decode_weights_workspace_size(
+        n, total, hq, hkv, d, split_keys), idx)
+    out = _output("out", out, (n, hq, d), q.dtype, idx)
+    lse = _output("lse", lse, (hq, n), torch.float32, idx)
+    slopes = _slopes_for(alibi_slopes, hq, idx)
+    _launch(idx, "mea_decode_weights", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            table.data_ptr(), cu.data_ptr(), out.data_ptr(), lse.data_ptr(), weights.data_ptr(),
+            _ptr(prev_weights), width, n, nb, bs, table.size(1), total, max_k, hq, hkv, d,
+            _scale_for(scale, d), _ptr(slopes), code, ws.data_ptr(), ws_bytes, int(split_keys))
     return out, lse, weights
 
 
@@ -623,33 +673,30 @@ def attention_packed_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor
     ``[n_seqs, Hkv, >= max_seqlen_k]``, summed over the heads of a KV group and over the queries
     (``last_queries`` > 0: each segment's last ones only). Entries past a segment's keys are left as
     they were (zeros when ``weights`` is made here)."""
-    if q.dim() != 3 or k.dim() != 3 or k.shape[2] != q.shape[2]:
+    idx = _gpu_index(q)
+    if q.dim() != 3 or k.dim() != 3 or k.size(2) != q.size(2):
         raise MeaError(_lib.MEA_ERR_SHAPE, "q [T_q, Hq, D], k [T_k, Hkv, D]")
-    if q.dtype != k.dtype:
+    if q.dtype is not k.dtype:
         raise MeaError(_lib.MEA_ERR_DTYPE, "q and k must share one dtype")
-    if not q.is_cuda:
-        raise MeaError(_lib.MEA_ERR_DEVICE, "tensors must live on the GPU")
-    dev = q.device
-    _on_device(dev, k=k, lse=lse)
-    q, k, lse = q.contiguous(), k.contiguous(), lse.contiguous()
+    _same_gpu("k", k, idx)
+    _same_gpu("lse", lse, idx)
+    q, k, lse = _dense(q), _dense(k), _dense(lse)
     tq, hq, d = q.shape
-    tk, hkv, _ = k.shape
-    if tuple(lse.shape) != (hq, tq) or lse.dtype != torch.float32:
+    tk, hkv = k.size(0), k.size(1)
+    if lse.shape != (hq, tq) or lse.dtype is not torch.float32:
         raise MeaError(_lib.MEA_ERR_SHAPE, f"lse must be float32 [{hq}, {tq}]")
-    n = cu_seqlens_q.numel() - 1
-    cu_q = _check_cu("cu_seqlens_q", cu_seqlens_q, n + 1, dev)
-    cu_k = _check_cu("cu_seqlens_k", cu_seqlens_k, n + 1, dev)
+    n, max_k = cu_seqlens_q.numel() - 1, int(max_seqlen_k)
+    cu_q = _check_prefix("cu_seqlens_q", cu_seqlens_q, n + 1, idx)
+    cu_k = _check_prefix("cu_seqlens_k", cu_seqlens_k, n + 1, idx)
     if weights is None:
-        weights = torch.zeros((n, hkv, int(max_seqlen_k)), dtype=torch.float32, device=dev)
-    else:
-        _check_weights("weights", weights, n, hkv, int(max_seqlen_k), dev)
-    slopes = _slopes_for(alibi_slopes, hq, dev)
-    _launch(
-        dev, "mea_attention_weights",
-        _ptr(q), _ptr(k), _ptr(lse), _ptr(cu_q), _ptr(cu_k), _ptr(weights), weights.shape[2], n, tq,
-        tk, int(max_seqlen_q), int(max_seqlen_k), hq, hkv, d, 1.0 / math.sqrt(d) if scale is None
-        else float(scale), _lib.MEA_MASK_CAUSAL if causal else _lib.MEA_MASK_NONE, _ptr(slopes),
-        int(last_queries), _dtype_code(q.dtype))
+        weights = torch.zeros((n, hkv, max_k), dtype=torch.float32, device=q.device)
+    width = _check_weights("weights", weights, n, hkv, max_k, idx)
+    slopes = _slopes_for(alibi_slopes, hq, idx)
+    _launch(idx, "mea_attention_weights", q.data_ptr(), k.data_ptr(), lse.data_ptr(),
+            cu_q.data_ptr(), cu_k.data_ptr(), weights.data_ptr(), width, n, tq, tk,
+            int(max_seqlen_q), max_k, hq, hkv, d, _scale_for(scale, d),
+            _lib.MEA_MASK_CAUSAL if causal else _lib.MEA_MASK_NONE, _ptr(slopes),
+            int(last_queries), _dtype_code(q.dtype))
     return weights
 
 
@@ -668,30 +715,31 @@ def evict_paged(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch
     shape, out_cu_seqlens_k [n_seqs + 1])``: the kept keys' indices (then -1) and weights (then 0)
     and the new prefix sums. Afterwards a slot holds another token's key for each head, so ALiBi no
     longer applies."""
-    table, cu = _check_paged(k_cache, v_cache, block_table, cu_seqlens_k)
-    nb, bs, hkv, d = k_cache.shape
-    dev = k_cache.device
-    n = table.shape[0]
-    _check_weights("weights", weights, n, hkv, int(max_seqlen_k), dev)
-    out_k_cache = k_cache if out_k_cache is None else out_k_cache
-    out_v_cache = v_cache if out_v_cache is None else out_v_cache
-    for name, t in (("out_k_cache", out_k_cache), ("out_v_cache", out_v_cache)):
-        _check_buffer(name, t, (out_k_cache.shape[0], bs, hkv, d), k_cache.dtype, dev)
-    if out_table.dtype != torch.int32 or out_table.dim() != 2 or out_table.shape[0] != n:
+    idx, (nb, bs, hkv, d), code, table, cu = _check_paged(k_cache, v_cache, block_table,
+                                                          cu_seqlens_k)
+    n, max_blocks = table.shape
+    max_k, n_keep = int(max_seqlen_k), int(n_keep)
+    if n_keep < 1:
+        raise MeaError(_lib.MEA_ERR_SHAPE, "n_keep must be at least 1")
+    width = _check_weights("weights", weights, n, hkv, max_k, idx)
+    ko = k_cache if out_k_cache is None else out_k_cache
+    vo = v_cache if out_v_cache is None else out_v_cache
+    out_shape = (ko.size(0), bs, hkv, d)
+    _output("out_k_cache", ko, out_shape, k_cache.dtype, idx)
+    _output("out_v_cache", vo, out_shape, k_cache.dtype, idx)
+    if out_table.dtype is not torch.int32 or out_table.dim() != 2 or out_table.size(0) != n:
         raise MeaError(_lib.MEA_ERR_SHAPE, "out_table must be int32 [n_seqs, max_out_blocks]")
-    _on_device(dev, out_table=out_table)
-    out_table = out_table.contiguous()
-    n_keep = int(n_keep)
-    kept = _output("kept", kept, (n, hkv, n_keep), torch.int32, dev)
-    out_weights = _output("out_weights", out_weights, (n, hkv, n_keep), torch.float32, dev)
-    out_cu = _output("out_cu_seqlens_k", out_cu_seqlens_k, (n + 1,), torch.int32, dev)
-    _launch(
-        dev, "mea_evict_paged",
-        _ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(cu), _ptr(weights), weights.shape[2],
-        _ptr(out_k_cache), _ptr(out_v_cache), _ptr(out_table), _ptr(kept), _ptr(out_weights),
-        _ptr(out_cu), n, nb, out_k_cache.shape[0], bs, table.shape[1], out_table.shape[1],
-        int(max_seqlen_k), hkv, d, n_keep, int(n_recent), _dtype_code(k_cache.dtype))
-    return kept, out_weights, out_cu
+    _same_gpu("out_table", out_table, idx)
+    out_table = _dense(out_table)
+    kept = _output("kept", kept, (n, hkv, n_keep), torch.int32, idx)
+    ow = _output("out_weights", out_weights, (n, hkv, n_keep), torch.float32, idx)
+    ocu = _output("out_cu_seqlens_k", out_cu_seqlens_k, (n + 1,), torch.int32, idx)
+    _launch(idx, "mea_evict_paged", k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(),
+            cu.data_ptr(), weights.data_ptr(), width, ko.data_ptr(), vo.data_ptr(),
+            out_table.data_ptr(), kept.data_ptr(), ow.data_ptr(), ocu.data_ptr(), n, nb,
+            out_shape[0], bs, max_blocks, out_table.size(1), max_k, hkv, d, n_keep,
+            int(n_recent), code)
+    return kept, ow, ocu
 
 
 def tree_mask(parents: Sequence[Sequence[int]], device=None) -> torch.Tensor:
@@ -728,29 +776,25 @@ def decode_tree_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     drafted token j when bit j % 32 of word j / 32 of its ``tree_mask`` row (int32 ``[T_q, words]``,
     :func:`tree_mask`) is set. ALiBi positions are the depths in the tree. Returns
     ``(out [T_q, Hq, D], lse [Hq, T_q])``."""
-    table, cu_k = _check_paged(k_cache, v_cache, block_table, cu_seqlens_k, q)
-    q = q.contiguous()
-    tq, hq, d = q.shape
-    nb, bs, hkv, _ = k_cache.shape
-    dev = q.device
-    n = table.shape[0]
-    cu_q = _check_cu("cu_seqlens_q", cu_seqlens_q, n + 1, dev)
-    if tree_mask.dtype != torch.int32 or tree_mask.dim() != 2 or tree_mask.shape[0] != tq:
+    idx, (nb, bs, hkv, d), code, table, cu_k = _check_paged(k_cache, v_cache, block_table,
+                                                            cu_seqlens_k, q)
+    q = _dense(q)
+    tq, hq, _ = q.shape
+    n = table.size(0)
+    cu_q = _check_prefix("cu_seqlens_q", cu_seqlens_q, n + 1, idx)
+    if tree_mask.dtype is not torch.int32 or tree_mask.dim() != 2 or tree_mask.size(0) != tq:
         raise MeaError(_lib.MEA_ERR_SHAPE, f"tree_mask must be int32 [{tq}, words]")
-    _on_device(dev, tree_mask=tree_mask)
-    tree_mask = tree_mask.contiguous()
-    if workspace is None:
-        workspace = torch.empty(decode_tree_workspace_size(hq, hkv, d), dtype=torch.uint8,
-                                device=dev)
-    out = _output("out", out, (tq, hq, d), q.dtype, dev)
-    lse = _output("lse", lse, (hq, tq), torch.float32, dev)
-    slopes = _slopes_for(alibi_slopes, hq, dev)
-    _launch(
-        dev, "mea_decode_tree",
-        _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(cu_q), _ptr(cu_k), _ptr(tree_mask),
-        _ptr(out), _ptr(lse), n, tq, int(max_seqlen_q), int(max_seqlen_k), tree_mask.shape[1], nb,
-        bs, table.shape[1], hq, hkv, d, 1.0 / math.sqrt(d) if scale is None else float(scale),
-        _ptr(slopes), _dtype_code(q.dtype), _ptr(workspace), _check_workspace(workspace, dev))
+    _same_gpu("tree_mask", tree_mask, idx)
+    mask = _dense(tree_mask)
+    ws, ws_bytes = _scratch(workspace, lambda: decode_tree_workspace_size(hq, hkv, d), idx)
+    out = _output("out", out, (tq, hq, d), q.dtype, idx)
+    lse = _output("lse", lse, (hq, tq), torch.float32, idx)
+    slopes = _slopes_for(alibi_slopes, hq, idx)
+    _launch(idx, "mea_decode_tree", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            table.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), mask.data_ptr(), out.data_ptr(),
+            lse.data_ptr(), n, tq, int(max_seqlen_q), int(max_seqlen_k), mask.size(1), nb, bs,
+            table.size(1), hq, hkv, d, _scale_for(scale, d), _ptr(slopes), code, ws.data_ptr(),
+            ws_bytes)
     return out, lse
 
 

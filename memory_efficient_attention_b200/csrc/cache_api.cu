@@ -232,11 +232,11 @@ int mea_select_blocks(const void* q, const void* bounds, const int32_t* block_ta
   p.n_first = n_first;
   p.n_last = n_last;
   p.max_live = static_cast<int>(live);
-  // CTAs per (request, head): as many as fill the SMs about once, and no more than have a round
-  // of 128 blocks to score.
+  // CTAs per (request, head): as many as fill the SMs about twice, and no more than have a round of
+  // 64 blocks to score.
   const long long pairs = static_cast<long long>(n_seqs) * n_heads_kv;
   int cs = 1;
-  while (cs < 8 && pairs * cs * 2 <= di.sms && live > 128ll * cs) cs *= 2;
+  while (cs < 8 && pairs * cs <= di.sms && live > 64ll * cs) cs *= 2;
   constexpr uint32_t max_smem = MEA_SELECT_MAX_BLOCKS * 4u;
   const uint32_t smem = static_cast<uint32_t>(live > 0 ? live : 1) * 4u;
   cudaLaunchConfig_t cfg{};

@@ -86,9 +86,11 @@ __global__ void __launch_bounds__(256) mea_key_bounds_kernel(const BoundsParams 
 }
 
 // ------------------------------------------------------------------------------------------
-// The k largest of n 32-bit keys by one CTA: radix selection, 8 bits a pass from the top. Returns
-// the key T of the k-th largest and in `ties` how many of the keys equal to T belong to the k
-// (the caller takes the lowest indices of them). 1 <= k <= n. `hist` holds 256 + 2 ints.
+// The k largest of n 32-bit keys by one CTA of NT threads: radix selection from the top, 11 bits a
+// pass. (Weights and scores share few exponents: 11 bits reach two bits into the mantissa, so that
+// a warp's counts spread over more bins than 8 bits would give them.) Returns the key T of the k-th
+// largest and in `ties` how many of the keys equal to T belong to the k (the caller takes the lowest
+// indices of them). 1 <= k <= n.
 // ------------------------------------------------------------------------------------------
 // Order-preserving image of an fp32 value (as unsigned; -0 equals +0). NaN ranks above all.
 __device__ __forceinline__ uint32_t rank_key(float x) {
@@ -96,88 +98,122 @@ __device__ __forceinline__ uint32_t rank_key(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
+// The value back from its rank key.
+__device__ __forceinline__ float rank_value(uint32_t k) {
+  return __uint_as_float(k == 0xFFFFFFFEu ? 0x7FFFFFFFu : (k & 0x80000000u) ? k ^ 0x80000000u : ~k);
+}
 constexpr uint32_t kRankAlways = 0xFFFFFFFFu;  // ranks above every value
 
-template <class Get>
-__device__ __forceinline__ uint32_t radix_select(Get get, int n, int k, int* hist, int& ties) {
-  const int tid = threadIdx.x, nt = blockDim.x;
-  uint32_t prefix = 0;
+struct SelectScratch {
+  int hist[2048];
+  int sum[2][32];
+  int bin, above;
+};
+
+// Exclusive sum over the CTA's warps of `v` (one value per warp, left in sum[] by the caller).
+template <int NT>
+__device__ __forceinline__ int warps_before(const int* sum) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int v = lane < NT / 32 ? sum[lane] : 0;
+  int incl = v;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, off);
+    if (lane >= off) incl += y;
+  }
+  return __shfl_sync(0xffffffffu, incl - v, warp);
+}
+
+template <int NT, class Get>
+__device__ __forceinline__ uint32_t radix_select(Get get, int n, int k, SelectScratch& sc,
+                                                 int& ties) {
+  constexpr int PER = 2048 / NT;  // bins per thread
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) sc.hist[tid * PER + i] = 0;
+  __syncthreads();
+  uint32_t prefix = 0, high = 0;
   int need = k;
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    for (int i = tid; i < 256; i += nt) hist[i] = 0;
-    __syncthreads();
-    const uint32_t high = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
-    for (int i = tid; i < n; i += nt) {
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+    const uint32_t mask = pass == 2 ? 1023u : 2047u;
+#pragma unroll 4
+    for (int i = tid; i < n; i += NT) {
       const uint32_t x = get(i);
-      if ((x & high) == prefix) atomicAdd(&hist[(x >> shift) & 255u], 1);
+      if ((x & high) == prefix) atomicAdd(&sc.hist[(x >> shift) & mask], 1);
     }
     __syncthreads();
-    // Warp 0: the bin, counted from the top, in which the need-th key falls.
-    if (tid < 32) {
-      int c[8], sum = 0;
+    // Thread tid takes the bins counted from the top, and clears them for the next pass.
+    int c[PER], sum = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = hist[255 - (tid * 8 + i)];
-        sum += c[i];
-      }
-      int incl = sum;
+    for (int i = 0; i < PER; ++i) {
+      int& h = sc.hist[2047 - (tid * PER + i)];
+      c[i] = h;
+      h = 0;
+      sum += c[i];
+    }
+    int incl = sum;
 #pragma unroll
-      for (int off = 1; off < 32; off <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, incl, off);
-        if (tid >= off) incl += y;
-      }
-      int above = incl - sum;
-      if (above < need && need <= incl) {
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+    if (lane == 31) sc.sum[0][warp] = incl;
+    __syncthreads();
+    int above = warps_before<NT>(sc.sum[0]) + incl - sum;
+    if (above < need && need <= above + sum) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (above < need && need <= above + c[i]) {
-            hist[256] = 255 - (tid * 8 + i);
-            hist[257] = above;
-          }
-          above += c[i];
+      for (int i = 0; i < PER; ++i) {
+        if (above < need && need <= above + c[i]) {
+          sc.bin = 2047 - (tid * PER + i);
+          sc.above = above;
         }
+        above += c[i];
       }
     }
     __syncthreads();
-    prefix |= static_cast<uint32_t>(hist[256]) << shift;
-    need -= hist[257];
-    __syncthreads();
+    prefix |= static_cast<uint32_t>(sc.bin) << shift;
+    need -= sc.above;
+    high |= mask << shift;
   }
   ties = need;
   return prefix;
 }
 
-// Writes the indices of the keys above T, and of the first `ties` keys equal to T, in ascending
-// order through put(place, index). `scan` holds 2 * 32 ints.
-template <class Get, class Put>
+// Hands the indices of the keys above T, and of the first `ties` keys equal to T, in ascending
+// order to put(place, index, key). A warp takes a contiguous part: it counts, the counts are added up
+// over the warps, then it places.
+template <int NT, class Get, class Put>
 __device__ __forceinline__ void compact_selected(Get get, Put put, int n, uint32_t T, int ties,
-                                                 int* scan) {
-  const int tid = threadIdx.x, nt = blockDim.x, lane = tid & 31, warp = tid >> 5;
-  const int nw = nt >> 5;
+                                                 SelectScratch& sc) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const unsigned below = (1u << lane) - 1u;
-  int base_gt = 0, base_eq = 0;  // keys above / equal before this round's range
-  for (int i0 = 0; i0 < n; i0 += nt) {
-    const int i = i0 + tid;
-    const uint32_t x = i < n ? get(i) : 0u;
-    const bool gt = i < n && x > T, eq = i < n && x == T;
-    const unsigned bg = __ballot_sync(0xffffffffu, gt), be = __ballot_sync(0xffffffffu, eq);
-    if (lane == 0) {
-      scan[warp] = __popc(bg);
-      scan[32 + warp] = __popc(be);
-    }
-    __syncthreads();
-    int pg = base_gt + __popc(bg & below), pe = base_eq + __popc(be & below);
-    for (int w = 0; w < nw; ++w) {
-      const int cg = scan[w], ce = scan[32 + w];
-      if (w < warp) {
-        pg += cg;
-        pe += ce;
-      }
-      base_gt += cg;
-      base_eq += ce;
-    }
-    if (gt || (eq && pe < ties)) put(pg + min(pe, ties), i);
-    __syncthreads();
+  const int part = ((n + NT - 1) / NT) * 32;
+  const int i0 = warp * part, i1 = min(n, i0 + part);
+  int gt = 0, eq = 0;
+  for (int b = i0; b < i1; b += 32) {
+    const uint32_t x = b + lane < i1 ? get(b + lane) : 0u;
+    gt += __popc(__ballot_sync(0xffffffffu, b + lane < i1 && x > T));
+    eq += __popc(__ballot_sync(0xffffffffu, b + lane < i1 && x == T));
+  }
+  if (lane == 0) {
+    sc.sum[0][warp] = gt;
+    sc.sum[1][warp] = eq;
+  }
+  __syncthreads();
+  gt = warps_before<NT>(sc.sum[0]);
+  eq = warps_before<NT>(sc.sum[1]);
+  for (int b = i0; b < i1; b += 32) {
+    const bool in = b + lane < i1;
+    const uint32_t x = in ? get(b + lane) : 0u;
+    const bool is_gt = in && x > T, is_eq = in && x == T;
+    const unsigned bg = __ballot_sync(0xffffffffu, is_gt);
+    const unsigned be = __ballot_sync(0xffffffffu, is_eq);
+    const int e = eq + __popc(be & below);
+    if (is_gt || (is_eq && e < ties)) put(gt + __popc(bg & below) + min(e, ties), b + lane, x);
+    gt += __popc(bg);
+    eq += __popc(be);
   }
 }
 
@@ -204,20 +240,18 @@ struct SelectParams {
   int max_live;        // bound on a request's blocks: rank keys in shared memory
 };
 
-constexpr int kSelThreads = 512;
+constexpr int kSelThreads = 256;
 
 template <bool BF16>
 __device__ __forceinline__ float half_f32(uint32_t w, int i) {
   const Half2<BF16> h = *reinterpret_cast<const Half2<BF16>*>(&w);
-  if constexpr (BF16)
-    return i ? __high2float(h) : __low2float(h);
-  else
-    return i ? __high2float(h) : __low2float(h);
+  return i ? __high2float(h) : __low2float(h);
 }
 
 // PIECES: 16-byte pieces of a block's two rows per lane (1 up to head dim 128, 2 above).
 template <bool BF16, int PIECES>
-__global__ void __launch_bounds__(kSelThreads) mea_select_blocks_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kSelThreads, PIECES == 1 ? 3 : 2)
+    mea_select_blocks_kernel(const SelectParams p) {
   namespace cg = cooperative_groups;
   auto cluster = cg::this_cluster();
   const int cs = static_cast<int>(cluster.num_blocks());
@@ -226,9 +260,8 @@ __global__ void __launch_bounds__(kSelThreads) mea_select_blocks_kernel(const Se
   const int b = pair / p.hkv, g = pair - b * p.hkv;
   const int R = p.hq / p.hkv;
   extern __shared__ __align__(16) uint32_t s_keys[];
-  __shared__ double s_w[2 * 256];  // [lo half: down][hi half: up]
-  __shared__ int s_hist[258];
-  __shared__ int s_scan[64];
+  __shared__ double s_w[2 * 256];  // [down][up]
+  __shared__ SelectScratch s_sc;
   const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
   const int nblk = min((L + p.block_size - 1) / p.block_size, min(p.max_blocks, p.max_live));
   int32_t* out = p.selected + (static_cast<size_t>(b) * p.hkv + g) * p.n_select;
@@ -238,10 +271,37 @@ __global__ void __launch_bounds__(kSelThreads) mea_select_blocks_kernel(const Se
       for (int i = tid; i < p.n_select; i += kSelThreads) out[i] = i < nblk ? i : -1;
     return;
   }
+  // The first CTA's shared memory must be live before the others write to it: each CTA says here
+  // that it runs, and waits for the others' word only before its first such write.
+  if (cs > 1) cluster.barrier_arrive();
+  const int np = p.dh / 4;  // 16-byte pieces of a block's ranges
+  const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
+  const uint4* bounds = static_cast<const uint4*>(p.bounds);
+  constexpr int U = 8;  // blocks in flight per warp
+  const int stride = cs * (kSelThreads / 32) * U;
+  int j0 = (cr * (kSelThreads / 32) + warp) * U;
+  auto block_id = [&](int j) { return (lane < U && j + lane < nblk) ? __ldg(row + j + lane) : -1; };
+  uint4 v[U][PIECES];
+  auto load = [&](int ids) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int id = __shfl_sync(0xffffffffu, ids, u);
+      const bool in = id >= 0 && id < p.num_blocks;
+      const uint4* src = bounds + (static_cast<size_t>(in ? id : 0) * p.hkv + g) * np;
+#pragma unroll
+      for (int c = 0; c < PIECES; ++c)
+        v[u][c] = (in && lane + 32 * c < np) ? __ldg(src + lane + 32 * c)
+                                             : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  load(block_id(j0));
+  int ids = block_id(j0 + stride);
+  // up and down, while the first blocks are on their way
   const Half1<BF16>* q =
       static_cast<const Half1<BF16>*>(p.q) + (static_cast<size_t>(b) * p.hq + g * R) * p.dh;
   for (int d = tid; d < p.dh; d += kSelThreads) {
     double up = 0.0, down = 0.0;
+#pragma unroll 8
     for (int h = 0; h < R; ++h) {
       const float x = static_cast<float>(q[static_cast<size_t>(h) * p.dh + d]);
       up += x > 0.f ? x : 0.f;
@@ -250,33 +310,16 @@ __global__ void __launch_bounds__(kSelThreads) mea_select_blocks_kernel(const Se
     s_w[d] = down;
     s_w[p.dh + d] = up;
   }
-  // The first CTA's shared memory must be live before others write to it.
-  cluster.sync();
-  uint32_t* keys = cluster.map_shared_rank(s_keys, 0);
-  const int np = p.dh / 4;  // 16-byte pieces of a block's ranges
+  __syncthreads();
   double w[PIECES][8];
 #pragma unroll
   for (int c = 0; c < PIECES; ++c)
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       w[c][i] = lane + 32 * c < np ? s_w[(lane + 32 * c) * 8 + i] : 0.0;
-  const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
-  const uint4* bounds = static_cast<const uint4*>(p.bounds);
-  constexpr int U = 8;  // blocks in flight per warp
-  const int warps = cs * (kSelThreads / 32);
-  for (int j0 = (cr * (kSelThreads / 32) + warp) * U; j0 < nblk; j0 += warps * U) {
-    const int my_id = (lane < U && j0 + lane < nblk) ? __ldg(row + j0 + lane) : -1;
-    uint4 v[U][PIECES];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int id = __shfl_sync(0xffffffffu, my_id, u);
-      const bool in = id >= 0 && id < p.num_blocks;
-      const uint4* src = bounds + (static_cast<size_t>(in ? id : 0) * p.hkv + g) * np;
-#pragma unroll
-      for (int c = 0; c < PIECES; ++c)
-        v[u][c] = (in && lane + 32 * c < np) ? __ldg(src + lane + 32 * c)
-                                             : make_uint4(0u, 0u, 0u, 0u);
-    }
+  if (cs > 1) cluster.barrier_wait();
+  uint32_t* keys = cs > 1 ? cluster.map_shared_rank(s_keys, 0) : s_keys;
+  for (; j0 < nblk; j0 += stride) {
     double s[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -289,6 +332,8 @@ __global__ void __launch_bounds__(kSelThreads) mea_select_blocks_kernel(const Se
           s[u] = fma(w[c][i], static_cast<double>(half_f32<BF16>(x[i >> 1], i & 1)), s[u]);
       }
     }
+    load(ids);
+    ids = block_id(j0 + 2 * stride);
     // Eight sums over the warp at once: each step halves how many a lane carries.
 #pragma unroll
     for (int half = U / 2, off = 16; half >= 1; half >>= 1, off >>= 1) {
@@ -302,22 +347,25 @@ __global__ void __launch_bounds__(kSelThreads) mea_select_blocks_kernel(const Se
         }
       }
     }
-    // (now lanes that agree in bits 2..4 of their index carry the same block)
+    // (bit 4 of the lane chose the upper four blocks, bit 3 the upper two of four, bit 2 the odd one)
     s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
     s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
-    const int u = (lane >> 2);  // bit 4 chose the upper four, bit 3 the upper two, bit 2 the odd one
-    if ((lane & 3) == 0 && j0 + u < nblk) {
-      const int j = j0 + u;
+    const int j = j0 + (lane >> 2);
+    if ((lane & 3) == 0 && j < nblk) {
       const bool always = j < p.n_first || j >= nblk - p.n_last;
       keys[j] = always ? kRankAlways : rank_key(static_cast<float>(s[0]));
     }
   }
-  cluster.sync();
+  if (cs > 1)
+    cluster.sync();
+  else
+    __syncthreads();
   if (cr != 0) return;
   int ties = 0;
   auto get = [&](int i) { return s_keys[i]; };
-  const uint32_t T = radix_select(get, nblk, p.n_select, s_hist, ties);
-  compact_selected(get, [&](int at, int i) { out[at] = i; }, nblk, T, ties, s_scan);
+  const uint32_t T = radix_select<kSelThreads>(get, nblk, p.n_select, s_sc, ties);
+  compact_selected<kSelThreads>(get, [&](int at, int i, uint32_t) { out[at] = i; }, nblk, T, ties,
+                                s_sc);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -353,8 +401,7 @@ __device__ __forceinline__ int evict_keys(const EvictParams& p, int b) {
 
 __global__ void __launch_bounds__(kEvictThreads) mea_evict_select_kernel(const EvictParams p) {
   extern __shared__ __align__(16) uint32_t s_keys[];
-  __shared__ int s_hist[258];
-  __shared__ int s_scan[64];
+  __shared__ SelectScratch s_sc;
   const int g = blockIdx.x % p.hkv, b = blockIdx.x / p.hkv;
   const int tid = threadIdx.x;
   const int L = evict_keys(p, b);
@@ -388,21 +435,29 @@ __global__ void __launch_bounds__(kEvictThreads) mea_evict_select_kernel(const E
   const int m = L - p.n_recent;       // keys that compete, for
   const int k = p.n_keep - p.n_recent;  // this many places (k < m)
   if (k > 0) {
-    auto put = [&](int at, int i) {
+    auto put = [&](int at, int i, uint32_t x) {
       kept[at] = i;
-      ow[at] = w[i];
+      ow[at] = rank_value(x);
     };
     int ties = 0;
     if (m <= p.smem_keys) {
-      for (int i = tid; i < m; i += kEvictThreads) s_keys[i] = rank_key(w[i]);
+      for (int i0 = tid; i0 < m; i0 += kEvictThreads * 8) {
+        float x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          x[u] = i0 + u * kEvictThreads < m ? __ldcs(w + i0 + u * kEvictThreads) : 0.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+          if (i0 + u * kEvictThreads < m) s_keys[i0 + u * kEvictThreads] = rank_key(x[u]);
+      }
       __syncthreads();
       auto get = [&](int i) { return s_keys[i]; };
-      const uint32_t T = radix_select(get, m, k, s_hist, ties);
-      compact_selected(get, put, m, T, ties, s_scan);
+      const uint32_t T = radix_select<kEvictThreads>(get, m, k, s_sc, ties);
+      compact_selected<kEvictThreads>(get, put, m, T, ties, s_sc);
     } else {
       auto get = [&](int i) { return rank_key(__ldg(w + i)); };
-      const uint32_t T = radix_select(get, m, k, s_hist, ties);
-      compact_selected(get, put, m, T, ties, s_scan);
+      const uint32_t T = radix_select<kEvictThreads>(get, m, k, s_sc, ties);
+      compact_selected<kEvictThreads>(get, put, m, T, ties, s_sc);
     }
   }
   for (int i = tid; i < p.n_recent; i += kEvictThreads) {
