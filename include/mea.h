@@ -301,20 +301,17 @@ int mea_select_blocks(const void* q, const void* bounds, const int32_t* block_ta
  * KV head) only: out and lse are those of a softmax over the keys of these blocks (positions for
  * ALiBi are the keys' own). Entries are block indices within the request, in any order; an entry
  * below 0 or past the request's blocks names no keys, and a block listed twice counts twice. A
- * list that names no key gives out = 0, lse = -inf.
+ * list that names no key gives out = 0, lse = -inf. n_select * block_size <= 2^30.
  *   workspace  at least mea_decode_selected_workspace_size(...) bytes, 256-byte aligned.
- *   split_keys listed keys per split-KV chunk, a multiple of 64 (rounded up to whole blocks); 0 =
- *              the library's choice, as for mea_decode_splitkv.
  */
 size_t mea_decode_selected_workspace_size(int n_seqs, int n_select, int block_size, int n_heads_q,
-                                          int n_heads_kv, int head_dim, int split_keys);
+                                          int n_heads_kv, int head_dim);
 int mea_decode_selected(const void* q, const void* k_cache, const void* v_cache,
                         const int32_t* block_table, const int32_t* cu_seqlens_k,
                         const int32_t* selected, void* out, float* lse, int n_seqs, int num_blocks,
                         int block_size, int max_blocks, int n_select, int n_heads_q,
                         int n_heads_kv, int head_dim, float scale, const float* alibi_slopes,
-                        int dtype, void* workspace, size_t workspace_bytes, int split_keys,
-                        void* stream);
+                        int dtype, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * mea_decode_weights — mea_decode_paged that also gives each key's attention weight, summed over
@@ -346,13 +343,16 @@ int mea_decode_weights(const void* q, const void* k_cache, const void* v_cache,
  * 256); lse DEVICE fp32 [n_heads_q, total_q], the forward's.
  *   weights       DEVICE fp32 [n_seqs, n_heads_kv, weights_stride], weights_stride >= max_seqlen_k.
  *   last_queries  0: all queries; n > 0: each segment's last n only.
+ *   workspace     at least mea_attention_weights_workspace_size(head_dim) bytes, 16-byte aligned.
  */
+size_t mea_attention_weights_workspace_size(int head_dim);
 int mea_attention_weights(const void* q, const void* k, const float* lse,
                           const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
                           float* weights, long long weights_stride, int n_seqs, int total_q,
                           int total_k, int max_seqlen_q, int max_seqlen_k, int n_heads_q,
                           int n_heads_kv, int head_dim, float scale, int mask_kind,
-                          const float* alibi_slopes, int last_queries, int dtype, void* stream);
+                          const float* alibi_slopes, int last_queries, int dtype,
+                          void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * mea_evict_paged — keeps n_keep keys of each (request, KV head): its last n_recent, and of the

@@ -42,7 +42,8 @@ __all__ = [
     "decode_splitkv_noalloc", "decode_workspace_size", "decode_tree_paged",
     "decode_tree_workspace_size", "tree_mask", "block_key_bounds", "select_blocks",
     "decode_paged_selected", "decode_selected_workspace_size", "decode_paged_weights",
-    "decode_weights_workspace_size", "attention_packed_weights", "evict_paged", "wait_selftest",
+    "decode_weights_workspace_size", "attention_packed_weights",
+    "attention_weights_workspace_size", "evict_paged", "wait_selftest",
     "alibi_slopes",
     "BlockDiagonalMask", "BlockDiagonalCausalMask", "LowerTriangularMask", "device_error",
     "set_wait_timeout_ns", "MeaError", "library_path",
@@ -586,17 +587,16 @@ def select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tens
 
 
 def decode_selected_workspace_size(n_seqs: int, n_select: int, block_size: int, n_heads_q: int,
-                                   n_heads_kv: int, head_dim: int, split_keys: int = 0) -> int:
+                                   n_heads_kv: int, head_dim: int) -> int:
     return int(_lib.load().mea_decode_selected_workspace_size(
-        n_seqs, n_select, block_size, n_heads_q, n_heads_kv, head_dim, split_keys))
+        n_seqs, n_select, block_size, n_heads_q, n_heads_kv, head_dim))
 
 
 def decode_paged_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                           block_table: torch.Tensor, cu_seqlens_k: torch.Tensor,
                           selected: torch.Tensor, alibi_slopes: Optional[torch.Tensor] = None,
                           scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
-                          split_keys: int = 0, out: Optional[torch.Tensor] = None,
-                          lse: Optional[torch.Tensor] = None):
+                          out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
     """:func:`decode_paged` over the blocks in ``selected`` (:func:`select_blocks`) only. Entries may
     be in any order; one below 0 or past the request's blocks names no keys, a block listed twice
     counts twice. Returns ``(out [n_seqs, Hq, D], lse [Hq, n_seqs])``."""
@@ -611,14 +611,14 @@ def decode_paged_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     selected = _dense(selected)
     n_select = selected.size(2)
     ws, ws_bytes = _scratch(workspace, lambda: decode_selected_workspace_size(
-        n, n_select, bs, hq, hkv, d, split_keys), idx)
+        n, n_select, bs, hq, hkv, d), idx)
     out = _output("out", out, (n, hq, d), q.dtype, idx)
     lse = _output("lse", lse, (hq, n), torch.float32, idx)
     slopes = _slopes_for(alibi_slopes, hq, idx)
     _launch(idx, "mea_decode_selected", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             table.data_ptr(), cu.data_ptr(), selected.data_ptr(), out.data_ptr(), lse.data_ptr(),
             n, nb, bs, table.size(1), n_select, hq, hkv, d, _scale_for(scale, d), _ptr(slopes),
-            code, ws.data_ptr(), ws_bytes, int(split_keys))
+            code, ws.data_ptr(), ws_bytes)
     return out, lse
 
 
@@ -662,12 +662,17 @@ def decode_paged_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     return out, lse, weights
 
 
+def attention_weights_workspace_size(head_dim: int) -> int:
+    return int(_lib.load().mea_attention_weights_workspace_size(head_dim))
+
+
 def attention_packed_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor,
                              cu_seqlens_q: torch.Tensor, cu_seqlens_k: torch.Tensor,
                              max_seqlen_q: int, max_seqlen_k: int, causal: bool = False,
                              alibi_slopes: Optional[torch.Tensor] = None,
                              scale: Optional[float] = None, last_queries: int = 0,
-                             weights: Optional[torch.Tensor] = None) -> torch.Tensor:
+                             weights: Optional[torch.Tensor] = None,
+                             workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The attention weight that a packed batch's queries put on its keys, for
     :func:`attention_packed` called with the same arguments (``lse`` is its result): ``weights`` fp32
     ``[n_seqs, Hkv, >= max_seqlen_k]``, summed over the heads of a KV group and over the queries
@@ -691,12 +696,13 @@ def attention_packed_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor
     if weights is None:
         weights = torch.zeros((n, hkv, max_k), dtype=torch.float32, device=q.device)
     width = _check_weights("weights", weights, n, hkv, max_k, idx)
+    ws, ws_bytes = _scratch(workspace, lambda: attention_weights_workspace_size(d), idx)
     slopes = _slopes_for(alibi_slopes, hq, idx)
     _launch(idx, "mea_attention_weights", q.data_ptr(), k.data_ptr(), lse.data_ptr(),
             cu_q.data_ptr(), cu_k.data_ptr(), weights.data_ptr(), width, n, tq, tk,
             int(max_seqlen_q), max_k, hq, hkv, d, _scale_for(scale, d),
             _lib.MEA_MASK_CAUSAL if causal else _lib.MEA_MASK_NONE, _ptr(slopes),
-            int(last_queries), _dtype_code(q.dtype))
+            int(last_queries), _dtype_code(q.dtype), ws.data_ptr(), ws_bytes)
     return weights
 
 

@@ -33,7 +33,8 @@ EXPORTS = ("mea_forward", "mea_forward_fp8", "mea_backward_workspace_size", "mea
            "mea_decode_workspace_size", "mea_decode_splitkv", "mea_decode_paged",
            "mea_decode_splitkv_noalloc", "mea_block_key_bounds", "mea_select_blocks",
            "mea_decode_selected_workspace_size", "mea_decode_selected",
-           "mea_decode_weights_workspace_size", "mea_decode_weights", "mea_attention_weights",
+           "mea_decode_weights_workspace_size", "mea_decode_weights",
+           "mea_attention_weights_workspace_size", "mea_attention_weights",
            "mea_evict_paged", "mea_decode_tree_workspace_size", "mea_decode_tree",
            "mea_status_string", "mea_device_error",
            "mea_set_wait_timeout_ns", "mea_wait_selftest", "mea_version")
@@ -78,15 +79,18 @@ def load() -> ctypes.CDLL:
     lib.mea_block_key_bounds.restype = ci
     lib.mea_select_blocks.argtypes = [vp] * 5 + [ci] * 12 + [vp]
     lib.mea_select_blocks.restype = ci
-    lib.mea_decode_selected_workspace_size.argtypes = [ci] * 7
+    lib.mea_decode_selected_workspace_size.argtypes = [ci] * 6
     lib.mea_decode_selected_workspace_size.restype = sz
-    lib.mea_decode_selected.argtypes = [vp] * 8 + [ci] * 8 + [cf, vp, ci, vp, sz, ci, vp]
+    lib.mea_decode_selected.argtypes = [vp] * 8 + [ci] * 8 + [cf, vp, ci, vp, sz, vp]
     lib.mea_decode_selected.restype = ci
     lib.mea_decode_weights_workspace_size.argtypes = [ci] * 6
     lib.mea_decode_weights_workspace_size.restype = sz
     lib.mea_decode_weights.argtypes = [vp] * 9 + [ll] + [ci] * 9 + [cf, vp, ci, vp, sz, ci, vp]
     lib.mea_decode_weights.restype = ci
-    lib.mea_attention_weights.argtypes = [vp] * 6 + [ll] + [ci] * 8 + [cf, ci, vp, ci, ci, vp]
+    lib.mea_attention_weights_workspace_size.argtypes = [ci]
+    lib.mea_attention_weights_workspace_size.restype = sz
+    lib.mea_attention_weights.argtypes = [vp] * 6 + [ll] + [ci] * 8 + [cf, ci, vp, ci, ci, vp, sz,
+                                                                       vp]
     lib.mea_attention_weights.restype = ci
     lib.mea_evict_paged.argtypes = [vp] * 5 + [ll] + [vp] * 6 + [ci] * 12 + [vp]
     lib.mea_evict_paged.restype = ci

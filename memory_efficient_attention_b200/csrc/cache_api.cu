@@ -56,33 +56,42 @@ bool decode_maps(CUtensorMap* tk, CUtensorMap* tv, const void* k, const void* v,
          encode_4d(tv, v, dtype, head_dim, n_heads_kv, block_size, num_blocks, 64, 1, rows, 1);
 }
 
+// The split kernel and what completes it. max_seqlen_k sizes the grid of the weights (DEC_WEIGHTS).
 template <int D, bool BF16, bool ALIBI, int MODE>
 int launch_split(const CUtensorMap& tk, const CUtensorMap& tv, const mea::DecParams& p, int grid,
-                 cudaStream_t stream) {
+                 int max_seqlen_k, cudaStream_t stream) {
   constexpr auto kern = mea::mea_decode_split_kernel<D, BF16, ALIBI, true, MODE>;
   constexpr uint32_t smem = mea::DecCfg<D, true>::SMEM_TOTAL;
+  constexpr int threads = mea::DecCfg<D, true>::THREADS;
   if (smem_attr_once<kern>(smem) != cudaSuccess) return MEA_ERR_CUDA;
   clear_stale_launch_error();
-  if (grid > 0) kern<<<grid, mea::DecCfg<D, true>::THREADS, smem, stream>>>(tk, tv, p);
-  if (cudaGetLastError() != cudaSuccess) return MEA_ERR_CUDA;
-  const dim3 mgrid(p.n_seqs, p.hq / p.R);
   if constexpr (MODE == mea::DEC_SELECTED) {
-    if (p.n_chunks > 1) mea::mea_lse_merge_kernel<D, BF16, true><<<mgrid, 256, 0, stream>>>(p);
+    if (launch_dependent(kern, grid, threads, smem, stream, tk, tv, p) != cudaSuccess)
+      return MEA_ERR_CUDA;
+    if (grid > 1 && launch_dependent(mea::mea_selected_merge_kernel<D, BF16>, grid - 1, 256, 0,
+                                     stream, p, grid) != cudaSuccess)
+      return MEA_ERR_CUDA;
+    return MEA_OK;
   } else {
-    mea::mea_lse_merge_kernel<D, BF16><<<mgrid, 256, 0, stream>>>(p);
+    if (grid > 0) kern<<<grid, threads, smem, stream>>>(tk, tv, p);
+    if (cudaGetLastError() != cudaSuccess) return MEA_ERR_CUDA;
+    const dim3 wgrid(1 + (max_seqlen_k + 1023) / 1024, p.hq / p.R, p.n_seqs);
+    return launch_dependent(mea::mea_decode_weights_kernel<D, BF16>, wgrid, 256, 0, stream, p) ==
+                   cudaSuccess
+               ? MEA_OK
+               : MEA_ERR_CUDA;
   }
-  return cudaGetLastError() == cudaSuccess ? MEA_OK : MEA_ERR_CUDA;
 }
 
 template <int MODE>
 int launch_split_any(int head_dim, int dtype, const CUtensorMap& tk, const CUtensorMap& tv,
-                     const mea::DecParams& p, int grid, cudaStream_t s) {
+                     const mea::DecParams& p, int grid, int max_k, cudaStream_t s) {
   const bool bf = dtype == MEA_BF16, al = p.slopes != nullptr;
 #define MEA_SPLIT(DD)                                                                     \
-  return bf ? (al ? launch_split<DD, true, true, MODE>(tk, tv, p, grid, s)                \
-                  : launch_split<DD, true, false, MODE>(tk, tv, p, grid, s))              \
-            : (al ? launch_split<DD, false, true, MODE>(tk, tv, p, grid, s)               \
-                  : launch_split<DD, false, false, MODE>(tk, tv, p, grid, s))
+  return bf ? (al ? launch_split<DD, true, true, MODE>(tk, tv, p, grid, max_k, s)                \
+                  : launch_split<DD, true, false, MODE>(tk, tv, p, grid, max_k, s))              \
+            : (al ? launch_split<DD, false, true, MODE>(tk, tv, p, grid, max_k, s)               \
+                  : launch_split<DD, false, false, MODE>(tk, tv, p, grid, max_k, s))
   if (head_dim > 128) MEA_SPLIT(256);
   if (head_dim > 64) MEA_SPLIT(128);
   MEA_SPLIT(64);
@@ -111,40 +120,14 @@ void fill_decode(mea::DecParams& p, const void* q, void* out, float* lse, const 
   p.timeout_ns = g_timeout_ns.load();
 }
 
-// ------------------------------------------------------------------------------------------
-// Decode over chosen blocks: every request has the same number of chunks.
-// ------------------------------------------------------------------------------------------
-struct SelLayout {
-  int chunk = 0, n_chunks = 0;
-  long long slots = 0;
-  size_t lse_off = 0, total = 0;
-};
-
-bool selected_layout(int n_seqs, int n_select, int block_size, int hq, int hkv, int d,
-                     int split_keys, int sms, SelLayout& L) {
-  if (n_seqs < 1 || n_select < 1 || !block_size_ok(block_size) || hq < 1 || hkv < 1 || hq % hkv ||
-      !dec_head_dim_ok(d) || split_keys < 0 || split_keys % 64)
-    return false;
-  const long long keys = static_cast<long long>(n_select) * block_size;
-  const long long total = keys * n_seqs;
-  if (keys > (1 << 30)) return false;
-  const int n_hb = hq / decode_rb(hq / hkv);
-  int chunk = split_keys ? split_keys
-                         : auto_split_keys(static_cast<int>(total < (1ll << 30) ? total : 1ll << 30),
-                                           n_hb, sms);
-  // whole blocks, so that a list entry belongs to one chunk
-  if (chunk % block_size)
-    chunk = static_cast<int>((static_cast<long long>(chunk) + block_size - 1) / block_size *
-                             block_size);
-  L.chunk = chunk;
-  L.n_chunks = static_cast<int>((keys + chunk - 1) / chunk);
-  L.slots = static_cast<long long>(L.n_chunks) * n_seqs;
-  if (L.slots > (1ll << 30)) return false;
-  const size_t o = static_cast<size_t>(L.slots) * hq * padded_head_dim(d) * sizeof(float);
-  L.lse_off = align_up(o, 256);
-  L.total = L.n_chunks == 1 ? 256  // one chunk: its result is the answer
-                            : L.lse_off + align_up(static_cast<size_t>(L.slots) * hq * 4, 256);
-  return true;
+// Decode over chosen blocks: two partial ranges per CTA, the heads of one item each.
+size_t selected_ws_lse(int hq, int hkv, int d, int sms) {
+  return align_up(2 * static_cast<size_t>(sms) * decode_rb(hq / hkv) * padded_head_dim(d) *
+                      sizeof(float), 256);
+}
+size_t selected_ws(int hq, int hkv, int d, int sms) {
+  return selected_ws_lse(hq, hkv, d, sms) +
+         align_up(2 * static_cast<size_t>(sms) * decode_rb(hq / hkv) * sizeof(float), 256);
 }
 
 }  // namespace
@@ -266,14 +249,13 @@ int mea_select_blocks(const void* q, const void* bounds, const int32_t* block_ta
 }
 
 size_t mea_decode_selected_workspace_size(int n_seqs, int n_select, int block_size, int n_heads_q,
-                                          int n_heads_kv, int head_dim, int split_keys) {
-  DeviceInfo di;
-  const int sms = (current_device_info(di) == MEA_OK) ? di.sms : 148;
-  SelLayout L;
-  if (!selected_layout(n_seqs, n_select, block_size, n_heads_q, n_heads_kv, head_dim, split_keys,
-                       sms, L))
+                                          int n_heads_kv, int head_dim) {
+  if (n_seqs < 1 || n_select < 1 || !block_size_ok(block_size) || n_heads_q < 1 ||
+      n_heads_kv < 1 || n_heads_q % n_heads_kv || !dec_head_dim_ok(head_dim))
     return 0;
-  return L.total;
+  DeviceInfo di;
+  return selected_ws(n_heads_q, n_heads_kv, head_dim,
+                     current_device_info(di) == MEA_OK ? di.sms : 148);
 }
 
 int mea_decode_selected(const void* q, const void* k_cache, const void* v_cache,
@@ -281,14 +263,14 @@ int mea_decode_selected(const void* q, const void* k_cache, const void* v_cache,
                         const int32_t* selected, void* out, float* lse, int n_seqs, int num_blocks,
                         int block_size, int max_blocks, int n_select, int n_heads_q,
                         int n_heads_kv, int head_dim, float scale, const float* alibi_slopes,
-                        int dtype, void* workspace, size_t workspace_bytes, int split_keys,
-                        void* stream) {
+                        int dtype, void* workspace, size_t workspace_bytes, void* stream) {
   if (!q || !k_cache || !v_cache || !block_table || !cu_seqlens_k || !selected || !out)
     return MEA_ERR_NULL;
   if (int rc = check_cache(n_seqs, num_blocks, block_size, max_blocks, n_heads_kv, head_dim, dtype))
     return rc;
   if (n_heads_q < 1 || n_heads_q % n_heads_kv != 0) return MEA_ERR_HEADS;
-  if (n_select < 1 || split_keys < 0 || split_keys % 64) return MEA_ERR_SHAPE;
+  const long long keys = static_cast<long long>(n_select) * block_size;
+  if (n_select < 1 || keys > (1ll << 30)) return MEA_ERR_SHAPE;
   if (!std::isfinite(scale)) return MEA_ERR_SCALE;
   if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
       (lse && !aligned(lse, 4)) || !aligned(cu_seqlens_k, 4) || !aligned(block_table, 4) ||
@@ -297,28 +279,26 @@ int mea_decode_selected(const void* q, const void* k_cache, const void* v_cache,
   if (!workspace || !aligned(workspace, 256)) return MEA_ERR_WORKSPACE;
   DeviceInfo di;
   if (int rc = current_device_info(di); rc != MEA_OK) return rc;
-  SelLayout L;
-  if (!selected_layout(n_seqs, n_select, block_size, n_heads_q, n_heads_kv, head_dim, split_keys,
-                       di.sms, L))
-    return MEA_ERR_SHAPE;
-  if (workspace_bytes < L.total) return MEA_ERR_WORKSPACE;
+  if (workspace_bytes < selected_ws(n_heads_q, n_heads_kv, head_dim, di.sms))
+    return MEA_ERR_WORKSPACE;
   mea::DecParams p{};
   fill_decode(p, q, out, lse, cu_seqlens_k, block_table, alibi_slopes, n_seqs, num_blocks,
               block_size, max_blocks, n_heads_q, n_heads_kv, head_dim, scale);
   p.selected = selected;
   p.n_select = n_select;
-  p.n_chunks = L.n_chunks;
-  p.chunk = L.chunk;
-  p.n_slots = static_cast<int>(L.slots);
-  p.n_items = L.slots * p.n_hb;
+  p.item_tiles = static_cast<int>((keys + 63) / 64);
+  p.n_items = static_cast<long long>(n_seqs) * p.n_hb;
   p.ws_o = static_cast<float*>(workspace);
-  p.ws_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.lse_off);
+  p.ws_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                      selected_ws_lse(n_heads_q, n_heads_kv, head_dim, di.sms));
   CUtensorMap tk, tv;
   if (!decode_maps(&tk, &tv, k_cache, v_cache, dtype, head_dim, n_heads_kv, block_size, num_blocks,
                    p))
     return MEA_ERR_CUDA;
-  const int grid = static_cast<int>(p.n_items < di.sms ? p.n_items : di.sms);
-  return launch_split_any<mea::DEC_SELECTED>(head_dim, dtype, tk, tv, p, grid,
+  // At least two tiles a CTA: a CTA costs about as much as streaming two.
+  const long long half = (p.n_items * p.item_tiles + 1) / 2;
+  const int grid = static_cast<int>(half < di.sms ? half : di.sms);
+  return launch_split_any<mea::DEC_SELECTED>(head_dim, dtype, tk, tv, p, grid, 0,
                                              static_cast<cudaStream_t>(stream));
 }
 
@@ -381,13 +361,8 @@ int mea_decode_weights(const void* q, const void* k_cache, const void* v_cache,
                    p))
     return MEA_ERR_CUDA;
   const int grid = total_k > 0 ? static_cast<int>(p.n_items < di.sms ? p.n_items : di.sms) : 0;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (int rc = launch_split_any<mea::DEC_WEIGHTS>(head_dim, dtype, tk, tv, p, grid, s)) return rc;
-  if (max_seqlen_k == 0) return MEA_OK;
-  const dim3 wgrid((max_seqlen_k + 1023) / 1024, n_heads_kv, n_seqs);
-  clear_stale_launch_error();
-  mea::mea_decode_weights_kernel<64><<<wgrid, 256, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MEA_OK : MEA_ERR_CUDA;
+  return launch_split_any<mea::DEC_WEIGHTS>(head_dim, dtype, tk, tv, p, grid, max_seqlen_k,
+                                            static_cast<cudaStream_t>(stream));
 }
 
 int mea_evict_paged(const void* k_cache, const void* v_cache, const int32_t* block_table,
@@ -451,8 +426,11 @@ int mea_evict_paged(const void* k_cache, const void* v_cache, const int32_t* blo
   clear_stale_launch_error();
   sel<<<static_cast<unsigned>(pairs), mea::kEvictThreads, static_cast<size_t>(p.smem_keys) * 4,
         s>>>(p);
-  mea::mea_evict_copy_kernel<<<static_cast<unsigned>(copies), 256, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? MEA_OK : MEA_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return MEA_ERR_CUDA;
+  return launch_dependent(mea::mea_evict_copy_kernel, static_cast<unsigned>(copies), 256, 0, s,
+                          p) == cudaSuccess
+             ? MEA_OK
+             : MEA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -473,6 +473,7 @@ constexpr int kEvictRows = 64;
 
 __global__ void __launch_bounds__(256) mea_evict_copy_kernel(const EvictParams p) {
   __shared__ long long s_src[kEvictRows], s_dst[kEvictRows];  // 16-byte piece offsets, -1: none
+  pdl_wait();
   const int tiles = (p.n_keep + kEvictRows - 1) / kEvictRows;
   const long long item = blockIdx.x;
   const int tile = static_cast<int>(item % tiles);

@@ -58,7 +58,7 @@ struct DecParams {
   // DEC_SELECTED
   const int32_t* selected;  // [n_seqs, hq / R, n_select] block indices in the request, -1: none
   int n_select;
-  int n_chunks;             // chunks per request, ceil(n_select * block_size / chunk)
+  int item_tiles;           // 64-key tiles of an item (request, head block): all its list's keys
   // DEC_WEIGHTS
   float* ws_s;              // [n_slots, hq, chunk] scores in log2 units
   const float* prev;        // [n_seqs, hq / R, w_stride] or null
@@ -149,21 +149,47 @@ __device__ __forceinline__ int dec_chunk_start(const int32_t* cu, int b, int chu
   return acc;
 }
 
-// Warp-cooperative: keys of chunk `key0` of the (request b, KV head g) list, up to the end of its
-// last entry that names a block (entries after that load and add nothing).
-__device__ __forceinline__ int dec_selected_keys(const DecParams& p, int b, int g, int key0) {
+// DEC_SELECTED: every item (request, head block) has item_tiles 64-key tiles; all items' tiles form
+// one line, cut into equal ranges, one per CTA, so that the SMs end together whatever the number
+// of items. A range that covers a whole item writes its result; one that covers part of an item (at
+// most two per CTA) leaves a partial for mea_selected_merge_kernel.
+struct DecRange {
+  long long pos, end, start;
+  int T;
+  __device__ __forceinline__ void init(const DecParams& p, int grid, int cta) {
+    T = p.item_tiles;
+    const long long total = p.n_items * T;
+    const long long per = (total + grid - 1) / grid;
+    start = pos = per * cta;
+    end = min(total, pos + per);
+  }
+  // The next item, its tiles [t0, t1) and where its partial goes (-1: the whole item).
+  __device__ __forceinline__ bool next(long long& item, int& t0, int& t1, int& slot, int cta) {
+    if (pos >= end) return false;
+    item = pos / T;
+    t0 = static_cast<int>(pos - item * T);
+    t1 = static_cast<int>(min(static_cast<long long>(T), t0 + (end - pos)));
+    slot = (t0 == 0 && t1 == T) ? -1 : 2 * cta + (pos == start ? 0 : 1);
+    pos += t1 - t0;
+    return true;
+  }
+};
+
+// Warp-cooperative: keys of the (request b, KV head g) list from key0 on, up to key1 and the end of
+// the last entry that names a block (entries after that load and add nothing).
+__device__ __forceinline__ int dec_selected_keys(const DecParams& p, int b, int g, int key0,
+                                                 int key1) {
   const int lane = threadIdx.x & 31;
   const int e0 = key0 / p.block_size;
-  const int ne = min(p.chunk / p.block_size, p.n_select - e0);
-  const int32_t* list =
-      p.selected + (static_cast<size_t>(b) * (p.hq / p.R) + g) * p.n_select + e0;
+  const int e1 = min((key1 + p.block_size - 1) / p.block_size, p.n_select);
+  const int32_t* list = p.selected + (static_cast<size_t>(b) * (p.hq / p.R) + g) * p.n_select;
   int live = 0;
-  for (int i = lane; i < ne; i += 32)
+  for (int i = e0 + lane; i < e1; i += 32)
     if (__ldg(list + i) >= 0) live = i + 1;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1)
     live = max(live, __shfl_xor_sync(0xffffffffu, live, off));
-  return live * p.block_size;
+  return max(min(live * p.block_size, key1) - key0, 0);
 }
 
 // PAGED: K/V live in a block cache [num_blocks, block_size, Hkv, D] addressed through a per-request
@@ -206,29 +232,38 @@ __global__ void __launch_bounds__(160, 1)
     tma_prefetch_desc(&tm_v);
   }
   __syncthreads();
+  if constexpr (MODE != DEC_ALL) {
+    pdl_trigger();  // (the merge's CTAs may take the place of this kernel's as they end)
+    if constexpr (MODE == DEC_SELECTED) pdl_wait();  // the block choice may be still running
+  }
 
   if (warp == 4) {
     // ------------------------------------------------------------------ TMA producer
     uint32_t cnt = 0;
     bool ok = true;
-    for (long long lin = blockIdx.x; lin < p.n_items && ok; lin += gridDim.x) {
-      const int cid = static_cast<int>(lin / p.n_hb);
-      const int hb = static_cast<int>(lin - static_cast<long long>(cid) * p.n_hb);
-      int b, c;
+    DecRange range;
+    if constexpr (MODE == DEC_SELECTED) range.init(p, gridDim.x, blockIdx.x);
+    for (long long lin = blockIdx.x; (MODE == DEC_SELECTED || lin < p.n_items) && ok;
+         lin += gridDim.x) {
+      long long item = lin;
+      int t0 = 0, t1 = 0, slot = 0;
       if constexpr (MODE == DEC_SELECTED) {
-        b = cid / p.n_chunks;
-        c = cid - b * p.n_chunks;
-      } else {
+        if (!range.next(item, t0, t1, slot, blockIdx.x)) break;
+      }
+      const int cid = static_cast<int>(item / p.n_hb);
+      const int hb = static_cast<int>(item - static_cast<long long>(cid) * p.n_hb);
+      int b = cid, c = 0;
+      if constexpr (MODE != DEC_SELECTED) {
         dec_find_chunk(p.cu_k, p.n_seqs, p.chunk, cid, b, c);
         if (b < 0) break;  // flat chunk ids only grow along this CTA's sequence
       }
       const int k0 = __ldg(p.cu_k + b);
       const int L = __ldg(p.cu_k + b + 1) - k0;
-      const int key0 = c * p.chunk;
+      const int key0 = MODE == DEC_SELECTED ? t0 * C::BK : c * p.chunk;
       const int g = (hb * p.RB) / p.R;
       int nk;
       if constexpr (MODE == DEC_SELECTED)
-        nk = dec_selected_keys(p, b, g, key0);
+        nk = dec_selected_keys(p, b, g, key0, t1 * C::BK);
       else
         nk = min(p.chunk, L - key0);
       const int n_tiles = (nk + C::BK - 1) / C::BK;
@@ -331,22 +366,27 @@ __global__ void __launch_bounds__(160, 1)
     const int t4 = lane & 3;   // fragment column pair
     uint32_t cnt = 0, n_done = 0, m_cnt = 0;
     bool ok = true;
-    for (long long lin = blockIdx.x; lin < p.n_items && ok; lin += gridDim.x) {
-      const int cid = static_cast<int>(lin / p.n_hb);
-      const int hb = static_cast<int>(lin - static_cast<long long>(cid) * p.n_hb);
-      int b, c;
+    DecRange range;
+    if constexpr (MODE == DEC_SELECTED) range.init(p, gridDim.x, blockIdx.x);
+    for (long long lin = blockIdx.x; (MODE == DEC_SELECTED || lin < p.n_items) && ok;
+         lin += gridDim.x) {
+      long long item = lin;
+      int t0 = 0, t1 = 0, part = -1;
       if constexpr (MODE == DEC_SELECTED) {
-        b = cid / p.n_chunks;
-        c = cid - b * p.n_chunks;
-      } else {
+        if (!range.next(item, t0, t1, part, blockIdx.x)) break;
+      }
+      const int cid = static_cast<int>(item / p.n_hb);
+      const int hb = static_cast<int>(item - static_cast<long long>(cid) * p.n_hb);
+      int b = cid, c = 0;
+      if constexpr (MODE != DEC_SELECTED) {
         dec_find_chunk(p.cu_k, p.n_seqs, p.chunk, cid, b, c);
         if (b < 0) break;
       }
       const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
-      const int key0 = c * p.chunk;
+      const int key0 = MODE == DEC_SELECTED ? t0 * C::BK : c * p.chunk;
       int nk;
       if constexpr (MODE == DEC_SELECTED)
-        nk = dec_selected_keys(p, b, (hb * p.RB) / p.R, key0);
+        nk = dec_selected_keys(p, b, (hb * p.RB) / p.R, key0, t1 * C::BK);
       else
         nk = min(p.chunk, L - key0);
       const int n_tiles = (nk + C::BK - 1) / C::BK;
@@ -595,11 +635,10 @@ __global__ void __launch_bounds__(160, 1)
             }
           }
           const int head = hb * p.RB + row;
-          const size_t slot = static_cast<size_t>(cid) * p.hq + head;
+          size_t slot = static_cast<size_t>(cid) * p.hq + head;
           const int d = pass * C::MC + dc;
           if constexpr (MODE == DEC_SELECTED) {
-            // One chunk per request: this partial is the result (no merge is launched).
-            if (p.n_chunks == 1) {
+            if (part < 0) {  // the whole item: its result
               using OutT = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
               if (d < p.dh)
                 reinterpret_cast<OutT*>(p.out)[slot * p.dh + d] =
@@ -609,6 +648,7 @@ __global__ void __launch_bounds__(160, 1)
                     Lsum > 0.f ? (M + __log2f(Lsum)) * LN2 : -INFINITY;
               continue;
             }
+            slot = static_cast<size_t>(part) * p.RB + row;
           }
           p.ws_o[slot * D + d] = Lsum > 0.f ? acc / Lsum : 0.f;
           if (d == 0) p.ws_lse[slot] = Lsum > 0.f ? (M + __log2f(Lsum)) * LN2 : -INFINITY;
@@ -628,22 +668,19 @@ __global__ void __launch_bounds__(160, 1)
 
 // Merge kernel: one CTA per (request, KV group); lse = ln sum_c exp(lse_c),
 // out = sum_c exp(lse_c - lse) O_c, cast to the output dtype.
-// FIXED: every request has p.n_chunks chunks (DEC_SELECTED); otherwise its length gives them.
-template <int D, bool BF16, bool FIXED = false>
-__global__ void __launch_bounds__(256)
-    mea_lse_merge_kernel(const DecParams p) {
+// dec_merge does one (request b, KV group g) with a whole CTA.
+template <int D, bool BF16>
+__device__ __forceinline__ void dec_merge(const DecParams& p, int b, int g) {
   // One CTA per (request b, KV group g): the R heads of the group, all their chunk partials.
   //   warp w (heads w, w+8, ...): M = max_c lse_c, z = sum_c exp(lse_c - M) -> shared memory;
   //   then thread (head, 4 columns): O = sum_c exp(lse_c - M) O_c / z with float4 loads.
-  const int b = blockIdx.x;
-  const int g = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __shared__ int s_start;
   __shared__ float s_m[64], s_z[64];
   const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
-  const int n = FIXED ? p.n_chunks : (L + p.chunk - 1) / p.chunk;
+  const int n = (L + p.chunk - 1) / p.chunk;
   if (threadIdx.x < 32) {
-    const int st = FIXED ? b * p.n_chunks : dec_chunk_start(p.cu_k, b, p.chunk);
+    const int st = dec_chunk_start(p.cu_k, b, p.chunk);
     if (threadIdx.x == 0) s_start = st;
   }
   __syncthreads();
@@ -705,19 +742,83 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// Attention weights of a decode step: thread t of CTA (key range, KV head g, request b) takes one
-// key and adds exp2(score - lse) over the R heads of the group, in head order, to the key's
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256)
+    mea_lse_merge_kernel(const DecParams p) {
+  dec_merge<D, BF16>(p, blockIdx.x, blockIdx.y);
+}
+
+// DEC_SELECTED: joins the partials of the items that several CTAs shared. CTA c looks at the
+// boundary between the ranges of CTAs c and c + 1: when an item crosses it and no earlier one, warp w
+// joins rows w, w + 8, ...
+template <int D, bool BF16>
+__global__ void __launch_bounds__(256) mea_selected_merge_kernel(const DecParams p, int grid) {
+  pdl_wait();
+  const long long T = p.item_tiles, total = p.n_items * T;
+  const long long per = (total + grid - 1) / grid;
+  const long long pos = per * (blockIdx.x + 1);
+  if (pos >= total) return;
+  const long long item = pos / T, i0 = item * T;
+  if (i0 == pos || i0 < pos - per) return;  // not crossed here, or first crossed earlier
+  const int c0 = blockIdx.x, c1 = static_cast<int>((i0 + T - 1) / per);
+  // CTA c0's part is its first range only when the item starts there; later CTAs' always is.
+  const int skip = i0 == pos - per ? 0 : 1;
+  const int b = static_cast<int>(item / p.n_hb);
+  const int hb = static_cast<int>(item - static_cast<long long>(b) * p.n_hb);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  using OutT = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
+  for (int row = warp; row < p.RB; row += 8) {
+    auto slot = [&](int c) {
+      return (2 * static_cast<size_t>(c) + (c == c0 ? skip : 0)) * p.RB + row;
+    };
+    constexpr float LOG2E = 1.4426950408889634f;
+    float M = -INFINITY;
+    for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, p.ws_lse[slot(c)]);
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    float z = 0.f, acc[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+    if (M != -INFINITY) {
+#pragma unroll 4
+      for (int c = c0; c <= c1; ++c) {
+        const float w = ex2_approx((p.ws_lse[slot(c)] - M) * LOG2E);
+        z += w;
+        const float* o = p.ws_o + slot(c) * D + lane;
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) acc[i] = fmaf(w, o[i * 32], acc[i]);
+      }
+    }
+    const float inv = z > 0.f ? 1.f / z : 0.f;
+    const int head = hb * p.RB + row;
+    OutT* dst = reinterpret_cast<OutT*>(p.out) + (static_cast<size_t>(b) * p.hq + head) * p.dh;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+      if (i * 32 + lane < p.dh) dst[i * 32 + lane] = static_cast<OutT>(acc[i] * inv);
+    if (lane == 0 && p.lse)
+      p.lse[static_cast<size_t>(head) * p.n_seqs + b] = z > 0.f ? M + __logf(z) : -INFINITY;
+  }
+}
+
+// Merge and attention weights of a decode step, in one launch: CTA (0, g, b) merges the partial
+// outputs; thread t of CTA (1 + key range, KV head g, request b) takes four keys and adds exp2(score - lse) over the R heads of the group, in head order, to the key's
 // previous weight. The row's lse comes from its chunks' lse, as in the merge above.
 // Bound by memory: it reads the scores that the split kernel wrote (4 R bytes a key, part of
 // them still in L2) and reads and writes 4 bytes of weight a key.
-template <int R_MAX>
+template <int D, bool BF16>
 __global__ void __launch_bounds__(256)
     mea_decode_weights_kernel(const DecParams p) {
   constexpr float LOG2E = 1.4426950408889634f;
+  constexpr int R_MAX = 64;
   const int b = blockIdx.z, g = blockIdx.y;
+  pdl_wait();
+  if (blockIdx.x == 0) {
+    dec_merge<D, BF16>(p, b, g);
+    return;
+  }
   int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
   if (p.w_stride < L) L = static_cast<int>(p.w_stride);  // never past the row of weights
-  const int t0 = blockIdx.x * 1024;
+  const int t0 = (blockIdx.x - 1) * 1024;
   if (t0 >= L) return;
   __shared__ int s_start;
   __shared__ float s_lse[R_MAX];

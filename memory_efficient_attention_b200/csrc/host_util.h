@@ -156,6 +156,24 @@ cudaError_t smem_attr_once(uint32_t smem) {
 // call's launches reports only their own failures.
 inline void clear_stale_launch_error() { (void)cudaGetLastError(); }
 
+// Launches `kern` as the dependent of the stream's previous kernel: it may start before that one
+// has ended and calls pdl_wait before it touches anything that one reads or writes.
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem,
+                             cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
+}
+
 // 3-D / 4-D maps through the cache (same arguments as the uncached encoders).
 inline bool encode_3d(CUtensorMap* map, const void* base, int dtype, uint64_t d0, uint64_t d1,
                uint64_t d2, uint32_t b0, uint32_t b1, uint32_t b2) {

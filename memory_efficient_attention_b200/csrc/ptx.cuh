@@ -224,6 +224,16 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
                : "memory");
 }
 
+// Dependent launches on one stream: a kernel launched as the next one's dependent may start, up to
+// its pdl_wait, when every CTA of the kernel before it has called pdl_trigger or ended; pdl_wait
+// returns once that kernel has ended and its writes are visible.
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // L1 prefetch of the line holding addr (a hint).
 __device__ __forceinline__ void prefetch_l1(const void* addr) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(addr));

@@ -36,26 +36,32 @@ int launch_tree(const CUtensorMap& tk, const CUtensorMap& tv, const mea::TreePar
   if (smem_attr_once<kern>(C::SMEM_TOTAL) != cudaSuccess) return MEA_ERR_CUDA;
   clear_stale_launch_error();
   kern<<<grid, C::THREADS, C::SMEM_TOTAL, s>>>(tk, tv, p);
-  if (grid > 1)
-    mea::mea_tree_merge_kernel<D, BF16>
-        <<<dim3(static_cast<unsigned>(grid - 1), C::ROWS / 8), 256, 0, s>>>(p, grid);
-  return cudaGetLastError() == cudaSuccess ? MEA_OK : MEA_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return MEA_ERR_CUDA;
+  if (grid > 1 && launch_dependent(mea::mea_tree_merge_kernel<D, BF16>,
+                                   dim3(static_cast<unsigned>(grid - 1), C::ROWS / 8), 256, 0, s,
+                                   p, grid) != cudaSuccess)
+    return MEA_ERR_CUDA;
+  return MEA_OK;
 }
 
 template <int D, bool BF16, bool CAUSAL, bool ALIBI>
 int launch_weights(const CUtensorMap& tq, const CUtensorMap& tk, const mea::WeightsParams& p,
-                   dim3 grid, cudaStream_t s) {
+                   int grid, cudaStream_t s) {
   constexpr auto kern = mea::mea_weights_sm100_kernel<D, BF16, CAUSAL, ALIBI>;
   using C = mea::WeightsCfg<D>;
   if (smem_attr_once<kern>(C::SMEM_TOTAL) != cudaSuccess) return MEA_ERR_CUDA;
   clear_stale_launch_error();
   kern<<<grid, C::THREADS, C::SMEM_TOTAL, s>>>(tq, tk, p);
-  return cudaGetLastError() == cudaSuccess ? MEA_OK : MEA_ERR_CUDA;
+  if (cudaGetLastError() != cudaSuccess) return MEA_ERR_CUDA;
+  if (grid > 1 && launch_dependent(mea::mea_weights_merge_kernel<D, CAUSAL>, grid - 1, C::KT, 0,
+                                   s, p, grid) != cudaSuccess)
+    return MEA_ERR_CUDA;
+  return MEA_OK;
 }
 
 template <int D, bool BF16>
 int launch_weights_d(bool causal, const CUtensorMap& tq, const CUtensorMap& tk,
-                     const mea::WeightsParams& p, dim3 grid, cudaStream_t s) {
+                     const mea::WeightsParams& p, int grid, cudaStream_t s) {
   const bool al = p.slopes != nullptr;
   if (causal)
     return al ? launch_weights<D, BF16, true, true>(tq, tk, p, grid, s)
@@ -71,6 +77,12 @@ size_t tree_ws_lse(int d, int sms) {
 }
 size_t tree_ws(int d, int sms) {
   return tree_ws_lse(d, sms) + 2 * static_cast<size_t>(sms) * tree_rows(d) * sizeof(float);
+}
+
+// Keys per item of the prompt's weights, and two ranges of them per CTA.
+int weights_keys(int d) { return d > 128 ? mea::WeightsCfg<256>::KT : mea::WeightsCfg<128>::KT; }
+size_t weights_ws(int d, int sms) {
+  return 2 * static_cast<size_t>(sms) * weights_keys(d) * sizeof(float);
 }
 
 }  // namespace
@@ -169,21 +181,27 @@ int mea_decode_tree(const void* q, const void* k_cache, const void* v_cache,
 #undef MEA_TREE
 }
 
+size_t mea_attention_weights_workspace_size(int head_dim) {
+  if (!dec_head_dim_ok(head_dim)) return 0;
+  DeviceInfo di;
+  return weights_ws(head_dim, current_device_info(di) == MEA_OK ? di.sms : 148);
+}
+
 int mea_attention_weights(const void* q, const void* k, const float* lse,
                           const int32_t* cu_seqlens_q, const int32_t* cu_seqlens_k,
                           float* weights, long long weights_stride, int n_seqs, int total_q,
                           int total_k, int max_seqlen_q, int max_seqlen_k, int n_heads_q,
                           int n_heads_kv, int head_dim, float scale, int mask_kind,
-                          const float* alibi_slopes, int last_queries, int dtype, void* stream) {
-  if (!q || !k || !lse || !cu_seqlens_q || !cu_seqlens_k || !weights) return MEA_ERR_NULL;
+                          const float* alibi_slopes, int last_queries, int dtype,
+                          void* workspace, size_t workspace_bytes, void* stream) {
+  if (!cu_seqlens_q || !cu_seqlens_k || (total_q > 0 && (!q || !lse)) ||
+      (max_seqlen_k > 0 && (!k || !weights)))
+    return MEA_ERR_NULL;
   if (n_seqs < 1 || total_q < 0 || total_k < 0 || max_seqlen_q < 0 || max_seqlen_k < 0 ||
       max_seqlen_q > total_q || max_seqlen_k > total_k || weights_stride < max_seqlen_k ||
       last_queries < 0)
     return MEA_ERR_SHAPE;
   if (n_heads_q < 1 || n_heads_kv < 1 || n_heads_q % n_heads_kv != 0) return MEA_ERR_HEADS;
-  const long long tiles = (static_cast<long long>(max_seqlen_k) + 127) / 128;
-  if (tiles > 65535 || static_cast<long long>(n_seqs) * n_heads_kv > 0x7fffffffll)
-    return MEA_ERR_SHAPE;
   if (!dec_head_dim_ok(head_dim)) return MEA_ERR_HEAD_DIM;
   if (dtype != MEA_F16 && dtype != MEA_BF16) return MEA_ERR_DTYPE;
   if (mask_kind != MEA_MASK_NONE && mask_kind != MEA_MASK_CAUSAL) return MEA_ERR_MASK;
@@ -192,32 +210,45 @@ int mea_attention_weights(const void* q, const void* k, const float* lse,
       !aligned(cu_seqlens_k, 4) || !aligned(weights, 4) ||
       (alibi_slopes && !aligned(alibi_slopes, 4)))
     return MEA_ERR_ALIGN;
+  if (!workspace || !aligned(workspace, 16)) return MEA_ERR_WORKSPACE;
   DeviceInfo di;
   if (int rc = current_device_info(di); rc != MEA_OK) return rc;
+  if (workspace_bytes < weights_ws(head_dim, di.sms)) return MEA_ERR_WORKSPACE;
   if (max_seqlen_k == 0) return MEA_OK;
+  const int R = n_heads_q / n_heads_kv;
+  int log2_p = 0;
+  while (log2_p < 7 && R % (2 << log2_p) == 0) ++log2_p;
   mea::WeightsParams p{};
   p.lse = lse;
   p.cu_q = cu_seqlens_q;
   p.cu_k = cu_seqlens_k;
   p.slopes = alibi_slopes;
   p.weights = weights;
+  p.ws = static_cast<float*>(workspace);
   p.w_stride = weights_stride;
   p.n_seqs = n_seqs;
   p.total_q = total_q;
   p.hq = n_heads_q;
   p.hkv = n_heads_kv;
-  p.R = n_heads_q / n_heads_kv;
+  p.R = R;
   p.last = last_queries;
+  p.log2_p = log2_p;
   p.c1 = scale * 1.4426950408889634f;
   p.timeout_ns = g_timeout_ns.load();
   CUtensorMap tq, tk;
+  // (without queries nothing of the q map is read: any address of the right alignment serves)
   const uint64_t q_rows = total_q > 0 ? static_cast<uint64_t>(total_q) : 1;
-  if (!encode_3d(&tq, q, dtype, head_dim, n_heads_q, q_rows, 64, 1, 128) ||
+  if (!encode_3d(&tq, total_q > 0 ? q : k, dtype, head_dim, total_q > 0 ? n_heads_q : n_heads_kv,
+                 q_rows, 64, total_q > 0 ? 1u << log2_p : 1u, 128u >> log2_p) ||
       !encode_3d(&tk, k, dtype, head_dim, n_heads_kv, total_k, 64, 1, 128))
     return MEA_ERR_CUDA;
-  // Key tile 0 first: under a causal mask it has the most queries.
-  const dim3 grid(static_cast<unsigned>(n_seqs) * static_cast<unsigned>(n_heads_kv),
-                  static_cast<unsigned>(tiles));
+  // No more CTAs than steps.
+  const long long kt = weights_keys(head_dim), qt = 128 >> log2_p;
+  const double items = static_cast<double>(n_seqs) * n_heads_kv *
+                       ((static_cast<long long>(max_seqlen_k) + kt - 1) / kt);
+  const double steps = items * (R >> log2_p) *
+                       ((static_cast<long long>(max_seqlen_q) + qt - 1) / qt + 1);
+  const int grid = steps < di.sms ? static_cast<int>(steps) : di.sms;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool causal = mask_kind == MEA_MASK_CAUSAL, bf = dtype == MEA_BF16;
   if (head_dim > 128)

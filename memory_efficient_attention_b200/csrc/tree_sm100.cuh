@@ -291,6 +291,7 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
 
   static_assert(256 * C::REGS_SOFTMAX + 128 * C::REGS_OTHER <= 384 * 168, "register split");
   if (warp >= 8) {
@@ -642,6 +643,7 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(256) mea_tree_merge_kernel(const TreeParams p, int grid) {
   using C = TreeCfg<D>;
   constexpr int ROWS = C::ROWS;
+  pdl_wait();
   const long long total = tree_total<ROWS>(p);
   const long long per = (total + grid - 1) / grid;
   const long long pos = per * (blockIdx.x + 1);

@@ -6,15 +6,27 @@
 // with the forward's masks, ALiBi and log-sum-exps; only a prompt's last `last` queries count where
 // that is given. The score matrix is recomputed tile by tile and never stored.
 //
-// One CTA per (key tile of 128, KV head, segment): the scores are computed transposed, S^T = K Q^T
-// (tcgen05, M = 128 keys, N = 128 queries), so that a key is a TMEM lane and a thread's sum over
-// the queries needs no other thread. K stays in shared memory, Q tiles of the group's heads stream
-// past it. Two warpgroups take the steps in turn, one S buffer each; every sum has one order, so
-// the result is deterministic.
+// The scores are computed transposed, S^T = K Q^T (tcgen05, M = 128 keys, N = 128 columns), so that a
+// key is a TMEM lane and a thread's sum over the columns needs no other thread. A column is a (query,
+// head) pair: a Q tile holds 128 / P queries of P heads of one KV group (P the largest power of two
+// that divides the group), so that a short window of queries fills the tile with heads, and a causal
+// diagonal wastes 128 / P columns, not 128.
 //
-// Bound by the exponentials: a score costs 2 D flop on the tensor cores and one exp2, and an SM
-// does 16 exp2 a clock (1024 clocks for a 128 x 128 tile, whose product takes a quarter of that at
-// D = 128).
+// An item is (segment, KV head, KT keys): its K tiles stay in shared memory (the next item's arrive
+// meanwhile) and its Q tiles stream past, one a step; SUBS key tiles share each Q tile, since one
+// would need half again the L2's bandwidth to keep up. All items' steps form one line, cut into equal
+// ranges, one per persistent CTA (a causal prompt's early keys have the most steps, and a short
+// window has few items; both load every SM alike). A range that covers part of an item leaves its
+// sums in the workspace and a second kernel adds them in order: every sum has one order, so the
+// result is deterministic.
+//
+// Roles: warp 16 the tcgen05 issuer, warp 17 the TMA producer, warp 18 the columns' terms (log-sum-exp
+// and ALiBi), warpgroups 0-3 the sums: warpgroup w takes key tile w % SUBS and part w / SUBS of the
+// columns.
+//
+// Bound by the exponentials: a score costs 2 D flop on the tensor cores and one exp2, and an SM does
+// 16 exp2 a clock: 1024 clocks for a 128 x 128 tile, whose product takes 512 at D = 128. Six of sixteen
+// column pairs therefore take a degree-4 polynomial on the FMA pipes instead (see exp2_poly2).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -30,52 +42,278 @@ struct WeightsParams {
   const int32_t* cu_k;
   const float* slopes;
   float* weights;    // [n_seqs, hkv, w_stride]
+  float* ws;         // [2 grid, KT] sums of the ranges that cover part of an item
   long long w_stride;
   int n_seqs, total_q, hq, hkv, R, last;
+  int log2_p;        // P = 1 << log2_p heads in a Q tile
   float c1;          // scale * log2(e)
   unsigned long long timeout_ns;
 };
 
 template <int D>
 struct WeightsCfg {
+  static constexpr int SUBS = D == 256 ? 1 : 2;  // 128-key tiles per item
+  static constexpr int KT = 128 * SUBS;
+  static constexpr int PARTS = 4 / SUBS;         // column parts, one per warpgroup of a key tile
+  static constexpr int COLS = 128 / PARTS;
+  static constexpr int NBUF = 4 / SUBS;          // S buffers (512 TMEM columns in all)
   static constexpr int ATOMS = D / 64;
   static constexpr uint32_t ATOM_BYTES = 128 * 128;
   static constexpr uint32_t TILE_BYTES = 128 * D * 2;
-  static constexpr int NQ = 2;  // Q tiles in the ring
+  static constexpr int NK = D == 256 ? 1 : 2;    // items whose K is in shared memory
+  static constexpr int NQ = D == 64 ? 4 : 2;     // Q tiles in the ring
+  static constexpr int NT = 4;                   // steps whose column terms are in shared memory
   static constexpr uint32_t SMEM_K = 0;
-  static constexpr uint32_t SMEM_Q = TILE_BYTES;
-  static constexpr uint32_t SMEM_NL = SMEM_Q + NQ * TILE_BYTES;  // 8 warps x 128 row terms
-  static constexpr uint32_t SMEM_SUM = SMEM_NL + 8 * 512;        // 128 floats
-  static constexpr uint32_t SMEM_MISC = SMEM_SUM + 512;
+  static constexpr uint32_t SMEM_Q = NK * SUBS * TILE_BYTES;
+  static constexpr uint32_t SMEM_T = SMEM_Q + NQ * TILE_BYTES;   // NT x 3 x 128 floats
+  static constexpr uint32_t SMEM_SUM = SMEM_T + NT * 3 * 512;    // 3 warpgroups x 128 floats
+  static constexpr uint32_t SMEM_MISC = SMEM_SUM + 3 * 512;
   static constexpr uint32_t SMEM_TOTAL = SMEM_MISC + 256 + 1024;
   static_assert(SMEM_TOTAL <= 232448, "shared memory per CTA");
-  static constexpr int CTAS = D == 256 ? 1 : 2;  // per SM
-  static constexpr int THREADS = 320;
+  static constexpr int THREADS = 640;
 };
 
+// A CTA's range of one item's steps.
+struct WeightsFrag {
+  int seg, g, q0, lq, k0, lk, j0;  // segment, KV head, its rows, first key
+  int qbeg, nt;                    // first query, Q tiles per head block
+  int s0, s1;                      // steps [s0, s1); step s is head block s / nt, Q tile s % nt
+  bool whole, first;
+};
+
+struct WeightsSeq {
+  int q0, lq, k0, lk, items;
+  long long work;  // steps of the segment's items of one KV head
+};
+
+template <int KT, bool CAUSAL>
+__device__ __forceinline__ void weights_item(const WeightsParams& p, const WeightsSeq& s, int kt,
+                                             int& qbeg, int& nt) {
+  qbeg = p.last > 0 ? max(s.lq - p.last, 0) : 0;
+  if (CAUSAL) qbeg = max(qbeg, kt * KT - (s.lk - s.lq));  // the first query that sees its first key
+  const int qt = 128 >> p.log2_p;
+  // (an item that no query sees still has a step, which finds nothing, so that zeros are written)
+  nt = qbeg < s.lq ? (s.lq - qbeg + qt - 1) / qt : 1;
+}
+
+template <int KT, bool CAUSAL>
+__device__ __forceinline__ WeightsSeq weights_seq(const WeightsParams& p, int seg) {
+  WeightsSeq s;
+  s.q0 = __ldg(p.cu_q + seg);
+  s.lq = max(__ldg(p.cu_q + seg + 1) - s.q0, 0);
+  s.k0 = __ldg(p.cu_k + seg);
+  s.lk = max(__ldg(p.cu_k + seg + 1) - s.k0, 0);
+  s.items = (s.lk + KT - 1) / KT;
+  s.work = 0;
+  for (int kt = 0; kt < s.items; ++kt) {
+    int qbeg, nt;
+    weights_item<KT, CAUSAL>(p, s, kt, qbeg, nt);
+    s.work += static_cast<long long>(nt) * (p.R >> p.log2_p);
+  }
+  return s;
+}
+
+// Warp-cooperative: steps of all segments (all KV heads).
+template <int KT, bool CAUSAL>
+__device__ __forceinline__ long long weights_total(const WeightsParams& p) {
+  long long acc = 0;
+  for (int s = threadIdx.x & 31; s < p.n_seqs; s += 32)
+    acc += weights_seq<KT, CAUSAL>(p, s).work * p.hkv;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+  return acc;
+}
+
+// Warp-cooperative: the segment that step `pos` of the line belongs to, and its first step.
+template <int KT, bool CAUSAL>
+__device__ __forceinline__ int weights_find(const WeightsParams& p, long long pos,
+                                            long long& base) {
+  const int lane = threadIdx.x & 31;
+  long long acc = 0;
+  for (int b0 = 0; b0 < p.n_seqs; b0 += 32) {
+    const long long w =
+        b0 + lane < p.n_seqs ? weights_seq<KT, CAUSAL>(p, b0 + lane).work * p.hkv : 0;
+    long long incl = w;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, pos < acc + incl);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      base = acc + __shfl_sync(0xffffffffu, incl - w, src);
+      return b0 + src;
+    }
+    acc += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  base = acc;
+  return p.n_seqs;
+}
+
+// A CTA's walk over its range of the line (segments, then KV heads, then items).
+template <int KT, bool CAUSAL>
+struct WeightsWalk {
+  long long pos, end, start, base;  // base: first step of item (seg, g, kt)
+  int seg, g, kt, qbeg, nt, len;    // len: steps of the item
+  WeightsSeq s;
+  __device__ __forceinline__ void load_item(const WeightsParams& p) {
+    weights_item<KT, CAUSAL>(p, s, kt, qbeg, nt);
+    len = nt * (p.R >> p.log2_p);
+  }
+  // Moves to the item that holds step `pos` (at or after the current one).
+  __device__ __forceinline__ void advance(const WeightsParams& p) {
+    while (pos >= base + len) {
+      base += len;
+      if (++kt == s.items) {
+        kt = 0;
+        if (++g == p.hkv) {
+          g = 0;
+          do s = weights_seq<KT, CAUSAL>(p, ++seg);
+          while (s.items == 0);  // (ends: pos lies before the line's end)
+        }
+      }
+      load_item(p);
+    }
+  }
+  __device__ __forceinline__ void init(const WeightsParams& p, int grid, int cta) {
+    const long long total = weights_total<KT, CAUSAL>(p);
+    const long long per = (total + grid - 1) / grid;
+    start = pos = per * cta;
+    end = min(total, pos + per);
+    if (pos >= end) return;
+    seek(p, pos);
+  }
+  __device__ __forceinline__ void seek(const WeightsParams& p, long long at) {
+    pos = at;
+    seg = weights_find<KT, CAUSAL>(p, at, base);
+    s = weights_seq<KT, CAUSAL>(p, seg);
+    g = static_cast<int>((at - base) / s.work);
+    base += s.work * g;
+    kt = 0;
+    load_item(p);
+    advance(p);
+  }
+  __device__ __forceinline__ bool next(const WeightsParams& p, WeightsFrag& f) {
+    if (pos >= end) return false;
+    advance(p);
+    f.seg = seg;
+    f.g = g;
+    f.q0 = s.q0;
+    f.lq = s.lq;
+    f.k0 = s.k0;
+    f.lk = s.lk;
+    f.j0 = kt * KT;
+    f.qbeg = qbeg;
+    f.nt = nt;
+    f.s0 = static_cast<int>(pos - base);
+    f.s1 = static_cast<int>(min(static_cast<long long>(len), f.s0 + (end - pos)));
+    f.whole = f.s0 == 0 && f.s1 == len;
+    f.first = pos == start;
+    pos += f.s1 - f.s0;
+    return true;
+  }
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+// 2^e for a pair of values of at most about 100, on the FMA and integer pipes: e = n + f with n the nearest
+// integer (added as 1.5 * 2^23, which leaves n in the low mantissa bits), 2^f by the degree-4
+// polynomial of least relative error on [-1/2, 1/2] (2.7e-6 in fp32, 4e-8 on average), n added to
+// the exponent. Values below -126 give about 2^-126.
+__device__ __forceinline__ uint64_t exp2_poly2(uint64_t e) {
+  float e0, e1;
+  f2_unpack(e, e0, e1);
+  // (a NaN stays one up to here and comes out as a huge value, not as a weight)
+  e = f2_pack(max_nan(e0, -126.f), max_nan(e1, -126.f));
+  const uint64_t magic = f2_pack(12582912.f, 12582912.f);
+  const uint64_t z = f2_add(e, magic);
+  const uint64_t n = f2_add(z, f2_pack(-12582912.f, -12582912.f));
+  const uint64_t f = f2_fma(n, f2_pack(-1.f, -1.f), e);
+  uint64_t r = f2_pack(0.009570102207362652f, 0.009570102207362652f);
+  r = f2_fma(r, f, f2_pack(0.05591785907745361f, 0.05591785907745361f));
+  r = f2_fma(r, f, f2_pack(0.240247443318367f, 0.240247443318367f));
+  r = f2_fma(r, f, f2_pack(0.6931217908859253f, 0.6931217908859253f));
+  r = f2_fma(r, f, f2_pack(0.9999992847442627f, 0.9999992847442627f));
+  float r0, r1, z0, z1;
+  f2_unpack(r, r0, r1);
+  f2_unpack(z, z0, z1);
+  return f2_pack(__int_as_float(__float_as_int(r0) + (__float_as_int(z0) << 23)),
+                 __int_as_float(__float_as_int(r1) + (__float_as_int(z1) << 23)));
+}
+
+// Column pairs of 16 that take the polynomial.
+constexpr uint32_t kWeightsPoly = 0x4A52u;
+
+// Adds 2^score over 32 columns of one key to acc. x: the raw products; terms: shared memory, this
+// chunk's row terms (nl, and with ALiBi the slopes and, non-causal, the queries' positions); key: the
+// key's index in the item. EDGE: only columns [lo, hi) of the chunk count.
+template <bool CAUSAL, bool ALIBI, bool EDGE>
+__device__ __forceinline__ void weights_chunk(const uint32_t (&x)[32], uint32_t terms,
+                                              uint64_t c1x2, float key, int lo, int hi,
+                                              uint64_t (&acc)[4]) {
+  const uint64_t keyx2 = f2_pack(key, key);
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    uint64_t nl[2], sl[2] = {0ull, 0ull}, ps[2] = {0ull, 0ull};
+    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                 : "=l"(nl[0]), "=l"(nl[1])
+                 : "r"(terms + i * 4));
+    if constexpr (ALIBI)
+      asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                   : "=l"(sl[0]), "=l"(sl[1])
+                   : "r"(terms + 512 + i * 4));
+    if constexpr (ALIBI && !CAUSAL)
+      asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
+                   : "=l"(ps[0]), "=l"(ps[1])
+                   : "r"(terms + 1024 + i * 4));
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int c = i + 2 * u;
+      uint64_t e = f2_fma(f2_pack(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), c1x2, nl[u]);
+      if constexpr (ALIBI && CAUSAL) e = f2_fma(sl[u], keyx2, e);
+      if constexpr (ALIBI && !CAUSAL) {
+        float p0, p1;
+        f2_unpack(ps[u], p0, p1);
+        e = f2_fma(sl[u], f2_pack(-fabsf(p0 - key), -fabsf(p1 - key)), e);
+      }
+      uint64_t w;
+      if ((kWeightsPoly >> (c >> 1)) & 1u) {
+        w = exp2_poly2(e);
+      } else {
+        float e0, e1;
+        f2_unpack(e, e0, e1);
+        w = f2_pack(ex2_approx(e0), ex2_approx(e1));
+      }
+      if constexpr (EDGE) {  // (a column that does not count may hold anything)
+        float w0, w1;
+        f2_unpack(w, w0, w1);
+        w = f2_pack(c >= lo && c < hi ? w0 : 0.f, c + 1 >= lo && c + 1 < hi ? w1 : 0.f);
+      }
+      acc[(i >> 1 & 2) + u] = f2_add(acc[(i >> 1 & 2) + u], w);
+    }
+  }
+}
+
 template <int D, bool BF16, bool CAUSAL, bool ALIBI>
-__global__ void __launch_bounds__(320, WeightsCfg<D>::CTAS)
+__global__ void __launch_bounds__(640, 1)
     mea_weights_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
                              const __grid_constant__ CUtensorMap tm_k, const WeightsParams p) {
   using C = WeightsCfg<D>;
+  using Walk = WeightsWalk<C::KT, CAUSAL>;
   constexpr float LOG2E = 1.4426950408889634f;
-  const int seg = blockIdx.x / p.hkv, g = blockIdx.x - seg * p.hkv;
-  const int q0 = __ldg(p.cu_q + seg), lq = max(__ldg(p.cu_q + seg + 1) - q0, 0);
-  const int k0 = __ldg(p.cu_k + seg), lk = max(__ldg(p.cu_k + seg + 1) - k0, 0);
-  const int j0 = blockIdx.y * 128;
-  if (j0 >= lk) return;
-  const int off = lk - lq;  // key position of query 0
-  int qbeg = p.last > 0 ? max(lq - p.last, 0) : 0;
-  if (CAUSAL) qbeg = max(qbeg, j0 - off);  // the first query that sees key j0
-  const int nt = qbeg < lq ? (lq - qbeg + 127) / 128 : 0;
-  const int steps = nt * p.R;
-
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
   uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = smem_u32(smem);
-  constexpr int B_KF = 0, B_QF = 1, B_QE = B_QF + C::NQ, B_SF = B_QE + C::NQ, B_SE = B_SF + 2;
-  constexpr int B_CM = B_SE + 2, B_DR = B_CM + 1, N_BARS = B_DR + 1;
+  constexpr int B_KF = 0, B_KE = B_KF + C::NK, B_QF = B_KE + C::NK, B_QE = B_QF + C::NQ;
+  constexpr int B_SF = B_QE + C::NQ, B_SE = B_SF + C::NBUF, B_TF = B_SE + C::NBUF;
+  constexpr int B_TE = B_TF + C::NT, B_CF = B_TE + C::NT, B_CE = B_CF + 1, B_DR = B_CE + 1;
+  constexpr int N_BARS = B_DR + 1;
   static_assert(8 * N_BARS + 8 <= 256, "barrier region");
   const uint32_t bar0 = sbase + C::SMEM_MISC;
 #define BAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
@@ -86,84 +324,125 @@ __global__ void __launch_bounds__(320, WeightsCfg<D>::CTAS)
   const uint64_t tmo = p.timeout_ns;
   const unsigned ecode = KID_WEIGHTS << 8;
   if (threadIdx.x == 0) {
-    mbar_init(BAR(B_KF), 1);
+    for (int s = 0; s < C::NK; ++s) {
+      mbar_init(BAR(B_KF + s), 1);
+      mbar_init(BAR(B_KE + s), 1);
+    }
     for (int s = 0; s < C::NQ; ++s) {
       mbar_init(BAR(B_QF + s), 1);
       mbar_init(BAR(B_QE + s), 1);
     }
-    for (int h = 0; h < 2; ++h) {
-      mbar_init(BAR(B_SF + h), 1);
-      mbar_init(BAR(B_SE + h), 4);  // one elected arrival per warp
+    for (int s = 0; s < C::NBUF; ++s) {
+      mbar_init(BAR(B_SF + s), 1);
+      mbar_init(BAR(B_SE + s), 16);  // one elected arrival per warp
     }
-    mbar_init(BAR(B_CM), 4);
+    for (int s = 0; s < C::NT; ++s) {
+      mbar_init(BAR(B_TF + s), 1);
+      mbar_init(BAR(B_TE + s), 16);
+    }
+    mbar_init(BAR(B_CF), 4 * (4 - C::SUBS));  // warps of the parts after the first
+    mbar_init(BAR(B_CE), 4 * C::SUBS);        // warps of the first part
     mbar_init(BAR(B_DR), 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 8) {
-    tmem_alloc(smem_u32(tmem_slot), 256);
+  if (warp == 16) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  bool ok = true;
+  pdl_trigger();
 
-  if (warp == 9) {
+  if (warp == 17) {
     // ---------------------------------------------------------------- TMA producer
-    if (lane == 0 && steps > 0) {
-      mbar_arrive_expect_tx(BAR(B_KF), C::TILE_BYTES);
-#pragma unroll
-      for (int a = 0; a < C::ATOMS; ++a)
-        tma_load_3d(sbase + C::SMEM_K + a * C::ATOM_BYTES, &tm_k, BAR(B_KF), a * 64, g, k0 + j0);
-      bool ok = true;
-      int t = 0, head = g * p.R, k = 0;
-      for (; k < steps; ++k) {
-        const uint32_t s = k % C::NQ;
-        ok = mbar_wait(BAR(B_QE + s), ((k / C::NQ) & 1u) ^ 1u, abort_flag, tmo, ecode | 1);
+    Walk w;
+    w.init(p, gridDim.x, blockIdx.x);
+    if (lane == 0) {
+      WeightsFrag f;
+      uint32_t n_frag = 0, k = 0;
+      while (ok && w.next(p, f)) {
+        const uint32_t kb = n_frag % C::NK;
+        ok = mbar_wait(BAR(B_KE + kb), ((n_frag / C::NK) & 1u) ^ 1u, abort_flag, tmo, ecode | 1);
         if (!ok) break;
-        mbar_arrive_expect_tx(BAR(B_QF + s), C::TILE_BYTES);
+        mbar_arrive_expect_tx(BAR(B_KF + kb), C::SUBS * C::TILE_BYTES);
 #pragma unroll
-        for (int a = 0; a < C::ATOMS; ++a)
-          tma_load_3d(sbase + C::SMEM_Q + s * C::TILE_BYTES + a * C::ATOM_BYTES, &tm_q,
-                      BAR(B_QF + s), a * 64, head, q0 + qbeg + t * 128);
-        if (++t == nt) {
-          t = 0;
-          ++head;
+        for (int h = 0; h < C::SUBS; ++h)
+#pragma unroll
+          for (int a = 0; a < C::ATOMS; ++a)
+            tma_load_3d(sbase + C::SMEM_K + (kb * C::SUBS + h) * C::TILE_BYTES + a * C::ATOM_BYTES,
+                        &tm_k, BAR(B_KF + kb), a * 64, f.g, f.k0 + f.j0 + h * 128);
+        ++n_frag;
+        int hb = f.s0 / f.nt, t = f.s0 - hb * f.nt;
+        for (int st = f.s0; st < f.s1; ++st, ++k) {
+          const uint32_t s = k % C::NQ;
+          ok = mbar_wait(BAR(B_QE + s), ((k / C::NQ) & 1u) ^ 1u, abort_flag, tmo, ecode | 2);
+          if (!ok) break;
+          mbar_arrive_expect_tx(BAR(B_QF + s), C::TILE_BYTES);
+#pragma unroll
+          for (int a = 0; a < C::ATOMS; ++a)
+            tma_load_3d(sbase + C::SMEM_Q + s * C::TILE_BYTES + a * C::ATOM_BYTES, &tm_q,
+                        BAR(B_QF + s), a * 64, f.g * p.R + (hb << p.log2_p),
+                        f.q0 + f.qbeg + t * (128 >> p.log2_p));
+          if (++t == f.nt) {
+            t = 0;
+            ++hb;
+          }
         }
       }
       if (!ok) {
         // Let the loads already issued land before the CTA's shared memory goes away.
         volatile int never = 0;
-        for (int s = 0; s < C::NQ && s < k; ++s) {
-          const int last = k - 1 - ((k - 1 - s) % C::NQ);
+        for (uint32_t s = 0; s < C::NQ && s < k; ++s) {
+          const uint32_t last = k - 1 - ((k - 1 - s) % C::NQ);
           mbar_wait(BAR(B_QF + s), (last / C::NQ) & 1u, &never, tmo, ecode | 15);
         }
-        mbar_wait(BAR(B_KF), 0, &never, tmo, ecode | 15);
+        for (uint32_t s = 0; s < C::NK && s < n_frag; ++s) {
+          const uint32_t last = n_frag - 1 - ((n_frag - 1 - s) % C::NK);
+          mbar_wait(BAR(B_KF + s), (last / C::NK) & 1u, &never, tmo, ecode | 15);
+        }
       }
     }
     __syncwarp();
-  } else if (warp == 8) {
+  } else if (warp == 16) {
     // ---------------------------------------------------------------- tcgen05 issuer
-    if (lane == 0 && steps > 0) {
+    Walk w;
+    w.init(p, gridDim.x, blockIdx.x);
+    if (lane == 0) {
       constexpr uint32_t IDESC = umma_idesc_f16(BF16, 128, 128, false, false);
-      bool ok = mbar_wait(BAR(B_KF), 0, abort_flag, tmo, ecode | 2);
-      for (int k = 0; k < steps && ok; ++k) {
-        const uint32_t s = k % C::NQ, h = k & 1;
-        ok = mbar_wait(BAR(B_QF + s), (k / C::NQ) & 1u, abort_flag, tmo, ecode | 3);
+      WeightsFrag f;
+      uint32_t n_frag = 0, k = 0;
+      while (ok && w.next(p, f)) {
+        const uint32_t kb = n_frag % C::NK;
+        ok = mbar_wait(BAR(B_KF + kb), (n_frag / C::NK) & 1u, abort_flag, tmo, ecode | 3);
         if (!ok) break;
-        ok = mbar_wait_spin(BAR(B_SE + h), ((k >> 1) & 1u) ^ 1u, abort_flag, tmo, ecode | 4);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t qb = sbase + C::SMEM_Q + s * C::TILE_BYTES;
+        ++n_frag;
+        for (int st = f.s0; st < f.s1; ++st, ++k) {
+          const uint32_t s = k % C::NQ, b = k % C::NBUF;
+          ok = mbar_wait(BAR(B_QF + s), (k / C::NQ) & 1u, abort_flag, tmo, ecode | 4);
+          if (!ok) break;
+          ok = mbar_wait_spin(BAR(B_SE + b), ((k / C::NBUF) & 1u) ^ 1u, abort_flag, tmo,
+                              ecode | 5);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t qb = sbase + C::SMEM_Q + s * C::TILE_BYTES;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * C::ATOM_BYTES + (kk & 3) * 32;
-          mma_ss(tmem + h * 128, umma_desc_sw128(sbase + C::SMEM_K + o, 16, 1024),
-                 umma_desc_sw128(qb + o, 16, 1024), IDESC, kk > 0 ? 1u : 0u);
+          for (int h = 0; h < C::SUBS; ++h) {
+            const uint32_t kbase = sbase + C::SMEM_K + (kb * C::SUBS + h) * C::TILE_BYTES;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t o = (kk >> 2) * C::ATOM_BYTES + (kk & 3) * 32;
+              mma_ss(tmem + (b * C::SUBS + h) * 128, umma_desc_sw128(kbase + o, 16, 1024),
+                     umma_desc_sw128(qb + o, 16, 1024), IDESC, kk > 0 ? 1u : 0u);
+            }
+          }
+          mma_commit(BAR(B_SF + b));
+          mma_commit(BAR(B_QE + s));
+          if (st == f.s1 - 1) mma_commit(BAR(B_KE + kb));
         }
-        mma_commit(BAR(B_SF + h));
-        mma_commit(BAR(B_QE + s));
       }
       // Every MMA issued so far must finish before TMEM is released.
       mma_commit(BAR(B_DR));
@@ -171,121 +450,176 @@ __global__ void __launch_bounds__(320, WeightsCfg<D>::CTAS)
       mbar_wait(BAR(B_DR), 0, &never, tmo, ecode | 14);
     }
     __syncwarp();
-  } else {
-    // ---------------------------------------------------------------- sums (thread = key)
-    const int h = warp >> 2;
-    const int r = threadIdx.x & 127;
-    const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + h * 128;
-    float* nl = reinterpret_cast<float*>(smem + C::SMEM_NL) + warp * 128;
-    const uint32_t nl_s = sbase + C::SMEM_NL + static_cast<uint32_t>(warp) * 512u;
-    const uint64_t c1x2 = f2_pack(p.c1, p.c1);
-    float sum = 0.f, comp = 0.f;  // running sum and what it lost
-    bool ok = true;
-    int t = h, head = g * p.R;    // this warpgroup's first step is number h
-    while (nt > 0 && t >= nt) {
-      t -= nt;
-      ++head;
-    }
-    for (int k = h; k < steps; k += 2) {
-      const int qt = qbeg + t * 128;
-      const int cols = min(lq - qt, 128);  // queries of the tile that exist
-      float slope2 = 0.f;
-      if constexpr (ALIBI) slope2 = __ldg(p.slopes + head) * LOG2E;
-      // Row terms: column c adds nl[c] = -lse2 (causal ALiBi: - slope2 (p_i - j0) as well, so that
-      // the key's own term is small too).
-      __syncwarp();
+  } else if (warp == 18) {
+    // ---------------------------------------------------------------- column terms
+    //   nl[c] = -lse2 (causal ALiBi: - slope2 (p_c - j0) as well: with the key's own + slope2 key the
+    //   terms stay small where weights are not), sl[c] = slope2, ps[c] = p_c - j0.
+    Walk w;
+    w.init(p, gridDim.x, blockIdx.x);
+    WeightsFrag f;
+    uint32_t k = 0;
+    while (ok && w.next(p, f)) {
+      int hb = f.s0 / f.nt, t = f.s0 - hb * f.nt;
+      for (int st = f.s0; st < f.s1; ++st, ++k) {
+        const uint32_t s = k % C::NT;
+        float nl[4], sl[4], ps[4];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int c = u * 32 + lane;
-        float v = -INFINITY;
-        if (c < cols) {
-          v = -LOG2E * __ldg(p.lse + static_cast<size_t>(head) * p.total_q + q0 + qt + c);
-          if (v == INFINITY) v = -INFINITY;  // (a row that attends to nothing)
-          if constexpr (ALIBI && CAUSAL) v -= slope2 * static_cast<float>(qt + c + off - j0);
-        }
-        nl[c] = v;
-      }
-      __syncwarp();
-      ok = mbar_wait(BAR(B_SF + h), (k >> 1) & 1u, abort_flag, tmo, ecode | 5);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      tc_fence_after();
-      const bool edge = cols < 128 || (CAUSAL && qt + off < j0 + 127);
-      const int clo = CAUSAL ? j0 + r - off - qt : 0;  // first column that sees this key
-      const float aj = ALIBI && CAUSAL ? slope2 * static_cast<float>(r) : 0.f;
-      const uint64_t ajx2 = f2_pack(aj, aj);
-      uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-#pragma unroll
-      for (int c4 = 0; c4 < 4; ++c4) {
-        if (c4 * 32 >= cols) break;
-        uint32_t x[32];
-        tmem_ld32(t_s + c4 * 32, x);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < 32; i += 4) {
-          uint64_t n0, n1;
-          asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
-                       : "=l"(n0), "=l"(n1)
-                       : "r"(nl_s + (c4 * 32 + i) * 4));
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const int c = c4 * 32 + i + 2 * u;
-            uint64_t e = f2_fma(f2_pack(__uint_as_float(x[i + 2 * u]),
-                                        __uint_as_float(x[i + 2 * u + 1])),
-                                c1x2, u ? n1 : n0);
-            if constexpr (ALIBI && CAUSAL) e = f2_add(e, ajx2);
-            float e0, e1;
-            f2_unpack(e, e0, e1);
-            if constexpr (ALIBI && !CAUSAL) {
-              const float d0 = static_cast<float>(qt + off - j0 - r);
-              e0 = fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), e0);
-              e1 = fmaf(-slope2, fabsf(d0 + static_cast<float>(c + 1)), e1);
+        for (int u = 0; u < 4; ++u) {
+          const int c = u * 32 + lane;
+          const int i = f.qbeg + t * (128 >> p.log2_p) + (c >> p.log2_p);
+          const int head = f.g * p.R + (hb << p.log2_p) + (c & ((1 << p.log2_p) - 1));
+          nl[u] = -INFINITY;
+          sl[u] = ps[u] = 0.f;
+          if (i < f.lq) {
+            nl[u] = -LOG2E * __ldg(p.lse + static_cast<size_t>(head) * p.total_q + f.q0 + i);
+            if (nl[u] == INFINITY) nl[u] = -INFINITY;  // (a row that attends to nothing)
+            if constexpr (ALIBI) {
+              sl[u] = __ldg(p.slopes + head) * LOG2E;
+              ps[u] = static_cast<float>(i + f.lk - f.lq - f.j0);
+              if (CAUSAL) nl[u] -= sl[u] * ps[u];
             }
-            if (edge) {
-              if (c < clo || c >= cols) e0 = -INFINITY;
-              if (c + 1 < clo || c + 1 >= cols) e1 = -INFINITY;
-            }
-            acc[(i >> 1 & 2) + u] =
-                f2_add(acc[(i >> 1 & 2) + u], f2_pack(ex2_approx(e0), ex2_approx(e1)));
           }
         }
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(B_SE + h));
-      float a0, a1;
-      f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a0, a1);
-      // Long prompts add thousands of tile sums: carry the rounding along.
-      const float y = (a0 + a1) - comp;
-      const float s2 = sum + y;
-      comp = (s2 - sum) - y;
-      sum = s2;
-      t += 2;
-      while (t >= nt) {
-        t -= nt;
-        ++head;
+        ok = mbar_wait(BAR(B_TE + s), ((k / C::NT) & 1u) ^ 1u, abort_flag, tmo, ecode | 6);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        float* dst = reinterpret_cast<float*>(smem + C::SMEM_T) + s * 384 + lane;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          dst[u * 32] = nl[u];
+          if constexpr (ALIBI) dst[128 + u * 32] = sl[u];
+          if constexpr (ALIBI && !CAUSAL) dst[256 + u * 32] = ps[u];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_TF + s));
+        if (++t == f.nt) {
+          t = 0;
+          ++hb;
+        }
       }
     }
-    // ---- the second warpgroup's sums join the first's
-    float* part = reinterpret_cast<float*>(smem + C::SMEM_SUM);
-    if (h == 1) {
-      part[r] = sum;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(BAR(B_CM));
-    } else {
-      if (ok) ok = mbar_wait(BAR(B_CM), 0, abort_flag, tmo, ecode | 6);
-      ok = __all_sync(0xffffffffu, ok);
-      if (ok && j0 + r < lk && j0 + r < p.w_stride)
-        p.weights[(static_cast<size_t>(seg) * p.hkv + g) * p.w_stride + j0 + r] = sum + part[r];
+  } else if (warp < 16) {
+    // ---------------------------------------------------------------- sums (thread = key)
+    const int wg = warp >> 2;
+    const int h = wg % C::SUBS, part = wg / C::SUBS;
+    const int r = threadIdx.x & 127;
+    const uint32_t t_lane =
+        tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + h * 128 + part * C::COLS;
+    const uint64_t c1x2 = f2_pack(p.c1, p.c1);
+    const float key = static_cast<float>(h * 128 + r);
+    float* sums = reinterpret_cast<float*>(smem + C::SMEM_SUM);
+    Walk w;
+    w.init(p, gridDim.x, blockIdx.x);
+    WeightsFrag f;
+    uint32_t n_frag = 0, k = 0;
+    while (ok && w.next(p, f)) {
+      float sum = 0.f, comp = 0.f;  // running sum and what it lost
+      const int off = f.lk - f.lq;
+      const int j = f.j0 + h * 128;  // first key of this warpgroup's tile
+      int t = f.s0 % f.nt;
+      for (int st = f.s0; st < f.s1; ++st, ++k) {
+        const int qi = f.qbeg + t * (128 >> p.log2_p);  // first query of the tile
+        if (++t == f.nt) t = 0;
+        // Columns [lo, hi) count for this key; every key of the tile sees all 128 off the edges.
+        const int hi = min((f.lq - qi) << p.log2_p, 128);
+        const int lo = CAUSAL ? max(j + r - off - qi, 0) << p.log2_p : 0;
+        const bool edge = hi < 128 || (CAUSAL && qi + off < j + 127);
+        const uint32_t b = k % C::NBUF, s = k % C::NT;
+        ok = mbar_wait(BAR(B_TF + s), (k / C::NT) & 1u, abort_flag, tmo, ecode | 7);
+        if (ok) ok = mbar_wait(BAR(B_SF + b), (k / C::NBUF) & 1u, abort_flag, tmo, ecode | 8);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t t_s = t_lane + b * (C::SUBS * 128);
+        const uint32_t terms = sbase + C::SMEM_T + s * 1536u + part * (C::COLS * 4u);
+        uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
+        uint32_t x[2][32];
+        tmem_ld32(t_s, x[0]);
+#pragma unroll
+        for (int c = 0; c < C::COLS / 32; ++c) {
+          tmem_wait_ld();
+          if (c + 1 < C::COLS / 32) tmem_ld32(t_s + (c + 1) * 32, x[(c + 1) & 1]);
+          const int c0 = part * C::COLS + c * 32;
+          if (!edge)
+            weights_chunk<CAUSAL, ALIBI, false>(x[c & 1], terms + c * 128, c1x2, key, 0, 32, acc);
+          else if (c0 < hi)
+            weights_chunk<CAUSAL, ALIBI, true>(x[c & 1], terms + c * 128, c1x2, key, lo - c0,
+                                               hi - c0, acc);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(BAR(B_SE + b));
+          mbar_arrive(BAR(B_TE + s));
+        }
+        float a0, a1;
+        f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a0, a1);
+        // Long prompts add thousands of tile sums: carry the rounding along.
+        const float y = (a0 + a1) - comp;
+        const float s2 = sum + y;
+        comp = (s2 - sum) - y;
+        sum = s2;
+      }
+      if (!ok) break;
+      // ---- the parts join, and the item's (or the range's) sums are written
+      if (part > 0) {
+        ok = mbar_wait(BAR(B_CE), (n_frag & 1u) ^ 1u, abort_flag, tmo, ecode | 9);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        sums[(wg - C::SUBS) * 128 + r] = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_CF));
+      } else {
+        ok = mbar_wait(BAR(B_CF), n_frag & 1u, abort_flag, tmo, ecode | 10);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+#pragma unroll
+        for (int q = 1; q < C::PARTS; ++q) sum += sums[(q * C::SUBS + h - C::SUBS) * 128 + r];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_CE));
+        const int row = h * 128 + r;
+        if (!f.whole)
+          p.ws[(2 * static_cast<size_t>(blockIdx.x) + (f.first ? 0 : 1)) * C::KT + row] = sum;
+        else if (f.j0 + row < f.lk && f.j0 + row < p.w_stride)
+          p.weights[(static_cast<size_t>(f.seg) * p.hkv + f.g) * p.w_stride + f.j0 + row] = sum;
+      }
+      ++n_frag;
     }
   }
 #undef BAR
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == 16) {
     tc_fence_after();
-    tmem_dealloc(tmem, 256);
+    tmem_dealloc(tmem, 512);
   }
+}
+
+// Adds up the sums of the items that several CTAs shared: CTA c looks at the boundary between the
+// ranges of CTAs c and c + 1; when an item crosses it and no earlier one, thread = key.
+template <int D, bool CAUSAL>
+__global__ void __launch_bounds__(WeightsCfg<D>::KT)
+    mea_weights_merge_kernel(const WeightsParams p, int grid) {
+  constexpr int KT = WeightsCfg<D>::KT;
+  pdl_wait();
+  const long long total = weights_total<KT, CAUSAL>(p);
+  const long long per = (total + grid - 1) / grid;
+  const long long pos = per * (blockIdx.x + 1);
+  if (pos >= total) return;
+  WeightsWalk<KT, CAUSAL> w;
+  w.seek(p, pos);
+  if (w.base == pos || w.base < pos - per) return;  // not crossed here, or first crossed earlier
+  const int c0 = blockIdx.x;
+  const int c1 = static_cast<int>((w.base + w.len - 1) / per);  // last CTA with a part
+  // CTA c0's part is its first range only when the item starts there; later CTAs' always is.
+  const int skip = w.base == pos - per ? 0 : 1;
+  const int row = threadIdx.x;
+  float sum = 0.f;
+  for (int c = c0; c <= c1; ++c)
+    sum += p.ws[(2 * static_cast<size_t>(c) + (c == c0 ? skip : 0)) * KT + row];
+  const int j = w.kt * KT + row;
+  if (j < w.s.lk && j < p.w_stride)
+    p.weights[(static_cast<size_t>(w.seg) * p.hkv + w.g) * p.w_stride + j] = sum;
 }
 
 }  // namespace mea

@@ -99,16 +99,16 @@ def test_select_blocks_ties_and_nan():
 
 
 # --------------------------------------------------------------------- decode over chosen blocks
-@pytest.mark.parametrize("lens,hq,hkv,d,dtype,bs,n_select,alibi,split", [
-    ([1], 1, 1, 8, FP, 16, 1, False, 0),
-    ([0, 17, 300, 1000], 8, 2, 64, BF, 16, 5, True, 0),
-    ([700, 40], 6, 2, 80, FP, 32, 9, False, 64),
-    ([2000, 129, 64], 12, 1, 128, BF, 16, 40, True, 128),
-    ([900, 1500], 8, 4, 256, BF, 64, 9, False, 0),
-    ([1000, 192], 40, 2, 128, FP, 192, 4, True, 64),
-    ([5000] * 40, 8, 4, 64, FP, 16, 33, False, 0),
+@pytest.mark.parametrize("lens,hq,hkv,d,dtype,bs,n_select,alibi", [
+    ([1], 1, 1, 8, FP, 16, 1, False),
+    ([0, 17, 300, 1000], 8, 2, 64, BF, 16, 5, True),
+    ([700, 40], 6, 2, 80, FP, 32, 9, False),
+    ([2000, 129, 64], 12, 1, 128, BF, 16, 40, True),
+    ([900, 1500], 8, 4, 256, BF, 64, 9, False),
+    ([1000, 192], 40, 2, 128, FP, 192, 4, True),
+    ([5000] * 40, 8, 4, 64, FP, 16, 33, False),
 ])
-def test_decode_selected(lens, hq, hkv, d, dtype, bs, n_select, alibi, split):
+def test_decode_selected(lens, hq, hkv, d, dtype, bs, n_select, alibi):
     c = ref.Cache(lens, hq, hkv, d, dtype, bs, 31)
     n = len(lens)
     q, slopes = randn((n, hq, d), 32, dtype), slopes_of(hq, alibi)
@@ -131,8 +131,7 @@ def test_decode_selected(lens, hq, hkv, d, dtype, bs, n_select, alibi, split):
             keys[-1].append([t for j in pick for t in range(j * bs, min(length, (j + 1) * bs))])
     kc, vc, table, cu = c.gpu()
     out, lse = mea.decode_paged_selected(q.cuda(), kc, vc, table, cu, sel.cuda(),
-                                         alibi_slopes=gpu(slopes), scale=d ** -0.5,
-                                         split_keys=split)
+                                         alibi_slopes=gpu(slopes), scale=d ** -0.5)
     o, m, z, _ = ref.decode(c, q, d ** -0.5, slopes, keys)
     ref.check_out(out.cpu(), lse.cpu(), o, m, z, dtype)
     assert mea.device_error() == 0
