@@ -16,8 +16,11 @@
 //
 // Roles and tensor-memory use follow the forward kernel: two softmax warpgroups, one per 128-row
 // sub-tile (thread = row = TMEM lane), an issuer warp that alternates the sub-tiles' Q K^T and P V
-// (tcgen05, fp32 in TMEM), a producer warp. The softmax warps also put Q into shared memory
-// (its rows are few and need not be a box of q).
+// (tcgen05, fp32 in TMEM), a producer warp, and a scheduler warp that hands the CTA's ranges, decoded,
+// to the others through a small queue in shared memory. The softmax warps also put Q into shared memory
+// (its rows are few and need not be a box of q). When an item's rows fit one sub-tile, both
+// warpgroups take those rows and every second key tile each, so that one's softmax still runs
+// beside the other's products; the first then joins the two O, which lie in the same TMEM lanes.
 //
 // Bound: with n_b R rows, a key costs 4 D bytes and 4 D n_b R flop; up to about 250 rows (bf16
 // peak over HBM rate) that is HBM-bound, beyond it the tensor cores are.
@@ -62,12 +65,15 @@ struct TreeCfg {
   static constexpr uint32_t SMEM_Q = 0;
   static constexpr uint32_t SMEM_KV = SUBS * TILE_BYTES;
   static constexpr uint32_t SMEM_POS = SMEM_KV + NS * TILE_BYTES;  // 8 warps x 128 floats
-  static constexpr uint32_t SMEM_MISC = SMEM_POS + 8 * 512;
-  static constexpr uint32_t SMEM_TOTAL = SMEM_MISC + 512 + 1024;
+  static constexpr uint32_t SMEM_ML = SMEM_POS + 8 * 512;  // the second warpgroup's (m, l) by row
+  static constexpr uint32_t SMEM_MISC = SMEM_ML + 1024;
+  static constexpr int QD = 4;                             // ranges in the queue, 64 bytes each
+  static constexpr uint32_t MISC_QUEUE = 512;
+  static constexpr uint32_t SMEM_TOTAL = SMEM_MISC + MISC_QUEUE + QD * 64 + 1024;
   static_assert(SMEM_TOTAL <= 232448, "shared memory per CTA");
   static constexpr int THREADS = 384;
-  static constexpr int REGS_SOFTMAX = 208;
-  static constexpr int REGS_OTHER = 80;
+  static constexpr int REGS_SOFTMAX = 216;
+  static constexpr int REGS_OTHER = 72;
   static constexpr uint32_t TM_O = 256;
 };
 
@@ -76,9 +82,15 @@ struct TreeFrag {
   int b, g, row0;        // request, KV head, first row of the item
   int q0, nq, ctx, L;    // first packed token, tokens, context keys, keys
   int t0, t1;            // tiles [t0, t1)
+  bool dual;             // one sub-tile's rows: the warpgroups take key tiles in turn
   bool whole;            // the range is the whole item
   bool first;            // the CTA's first range
 };
+
+// A range in the queue: 32-bit words at these places; flags 0 ends the list.
+enum : uint32_t { TQ_B = 0, TQ_G = 4, TQ_ROW0 = 8, TQ_Q0 = 12, TQ_NQ = 16, TQ_CTX = 20, TQ_L = 24,
+                  TQ_T0 = 28, TQ_T1 = 32, TQ_FLAGS = 36 };
+enum : int { TF_LIVE = 1, TF_DUAL = 2, TF_WHOLE = 4, TF_FIRST = 8 };
 
 struct TreeSeq {
   int q0, nq, L, tiles, parts;
@@ -166,6 +178,7 @@ struct TreeWalk {
     f.nq = s.nq;
     f.L = s.L;
     f.ctx = s.L - s.nq;
+    f.dual = ROWS == 256 && s.nq * p.R - f.row0 <= 128;
     f.whole = f.t0 == 0 && f.t1 == s.tiles;
     f.first = pos == start;
     pos += f.t1 - f.t0;
@@ -250,9 +263,10 @@ __global__ void __launch_bounds__(384, 1)
   const uint32_t q_s = sbase + C::SMEM_Q;
   const uint32_t kv_s0 = sbase + C::SMEM_KV;
   constexpr int B_QF = 0, B_QE = 1, B_KVF = 2, B_KVE = 2 + C::NS, B_SF = 2 + 2 * C::NS;
-  constexpr int B_PF = B_SF + 2, B_OF = B_PF + 2, B_OE = B_OF + 2, B_DR = B_OE + 2;
-  constexpr int N_BARS = B_DR + 1;
-  static_assert(8 * N_BARS + 8 <= 512, "barrier region");
+  constexpr int B_PF = B_SF + 2, B_OF = B_PF + 2, B_OE = B_OF + 2, B_ML = B_OE + 2;
+  constexpr int B_IF = B_ML + 1, B_IE = B_IF + C::QD;
+  constexpr int B_DR = B_IE + C::QD, N_BARS = B_DR + 1;
+  static_assert(8 * N_BARS + 8 <= C::MISC_QUEUE, "barrier region");
   const uint32_t bar0 = sbase + C::SMEM_MISC;
 #define BAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC + 8 * N_BARS);
@@ -275,6 +289,11 @@ __global__ void __launch_bounds__(384, 1)
       mbar_init(BAR(B_OF + h), 1);
       mbar_init(BAR(B_OE + h), 128);
     }
+    mbar_init(BAR(B_ML), 4);
+    for (int s = 0; s < C::QD; ++s) {
+      mbar_init(BAR(B_IF + s), 1);
+      mbar_init(BAR(B_IE + s), 2 + 4 * C::SUBS);  // producer, issuer, softmax warps
+    }
     mbar_init(BAR(B_DR), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -291,6 +310,7 @@ __global__ void __launch_bounds__(384, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  const uint32_t queue = sbase + C::SMEM_MISC + C::MISC_QUEUE;
   pdl_trigger();
 
   static_assert(256 * C::REGS_SOFTMAX + 128 * C::REGS_OTHER <= 384 * 168, "register split");
@@ -298,23 +318,31 @@ __global__ void __launch_bounds__(384, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
     if (warp == 9) {
       // -------------------------------------------------------------- TMA producer
-      TreeWalk<C::ROWS> w;
-      w.init(p);
-      TreeFrag f;
-      uint32_t cnt = 0;
+      uint32_t cnt = 0, n_frag = 0;
       bool ok = true;
       // One box of box_rows keys x 64 columns per lane (at most 8 x 4 boxes a tile).
       const int nbox = 128 / p.box_rows * C::ATOMS;
       const int piece = lane / C::ATOMS, atom = lane % C::ATOMS;
       const bool issuer = lane < nbox;
-      while (ok && w.next(p, f)) {
-        const int32_t* row = p.block_table + static_cast<size_t>(f.b) * p.max_blocks;
-        const int nblk = min((f.L + p.block_size - 1) / p.block_size, p.max_blocks);
-        const int n = f.t1 - f.t0;
+      while (true) {
+        const uint32_t e = queue + 64u * (n_frag % C::QD);
+        ok = mbar_wait(BAR(B_IF + n_frag % C::QD), (n_frag / C::QD) & 1u, abort_flag, tmo,
+                       ecode | 13);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok || lds_s32(e + TQ_FLAGS) == 0) break;
+        const int fg = lds_s32(e + TQ_G), ft1 = lds_s32(e + TQ_T1);
+        const int L = lds_s32(e + TQ_L);
+        const int32_t* row =
+            p.block_table + static_cast<size_t>(lds_s32(e + TQ_B)) * p.max_blocks;
+        const int nblk = min((L + p.block_size - 1) / p.block_size, p.max_blocks);
+        const int n = ft1 - lds_s32(e + TQ_T0);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_IE + n_frag % C::QD));
+        ++n_frag;
         // Tiles go from the last one down. A block past the request's last one takes id num_blocks,
         // which the TMA fills with zeros; ids are read three tiles ahead of their use.
         auto block_id = [&](int jj) {
-          const int blk = ((f.t1 - 1 - jj) * 128 + piece * p.box_rows) / p.block_size;
+          const int blk = ((ft1 - 1 - jj) * 128 + piece * p.box_rows) / p.block_size;
           return (issuer && jj < n && blk < nblk) ? __ldg(row + blk) : p.num_blocks;
         };
         int id_q[3];
@@ -325,7 +353,7 @@ __global__ void __launch_bounds__(384, 1)
           id_q[0] = id_q[1];
           id_q[1] = id_q[2];
           id_q[2] = block_id(jj + 3);
-          const int r0 = ((f.t1 - 1 - jj) * 128 + piece * p.box_rows) % p.block_size;
+          const int r0 = ((ft1 - 1 - jj) * 128 + piece * p.box_rows) % p.block_size;
 #pragma unroll 1
           for (int kv = 0; kv < 2; ++kv) {
             const uint32_t s = cnt % C::NS;
@@ -338,10 +366,11 @@ __global__ void __launch_bounds__(384, 1)
             if (issuer)
               tma_load_4d(kv_s0 + s * C::TILE_BYTES + atom * C::ATOM_BYTES +
                               static_cast<uint32_t>(piece * p.box_rows * 128),
-                          kv ? &tm_v : &tm_k, BAR(B_KVF + s), atom * 64, f.g, r0, id);
+                          kv ? &tm_v : &tm_k, BAR(B_KVF + s), atom * 64, fg, r0, id);
             ++cnt;
           }
         }
+        if (!ok) break;
       }
       if (!ok && lane == 0) {
         // Let the loads already issued land before the CTA's shared memory goes away.
@@ -354,40 +383,41 @@ __global__ void __launch_bounds__(384, 1)
       __syncwarp();
     } else if (warp == 8) {
       // -------------------------------------------------------------- tcgen05 issuer
-      TreeWalk<C::ROWS> w;
-      w.init(p);
       if (lane == 0) {
         constexpr uint32_t IDESC_QK = umma_idesc_f16(BF16, 128, 128, false, false);
         constexpr uint32_t IDESC_PV = umma_idesc_f16(BF16, 128, D, false, true);
-        TreeFrag f;
         uint32_t kv_cnt = 0, n_frag = 0;
         uint32_t pv_cnt[2] = {0, 0}, oe_cnt[2] = {0, 0};
         bool ok = true;
-        while (ok && w.next(p, f)) {
-          const int n = f.t1 - f.t0;
-          const int subs = (C::SUBS == 2 && f.nq * p.R - f.row0 > 128) ? 2 : 1;
+        while (ok) {
+          const uint32_t e = queue + 64u * (n_frag % C::QD);
+          ok = mbar_wait(BAR(B_IF + n_frag % C::QD), (n_frag / C::QD) & 1u, abort_flag, tmo,
+                         ecode | 16);
+          if (!ok) break;
+          const int flags = lds_s32(e + TQ_FLAGS);
+          if (flags == 0) break;
+          const int n = lds_s32(e + TQ_T1) - lds_s32(e + TQ_T0);
+          const bool dual = (flags & TF_DUAL) != 0;
+          mbar_arrive(BAR(B_IE + n_frag % C::QD));
           ok = mbar_wait(BAR(B_QF), n_frag & 1u, abort_flag, tmo, ecode | 6);
           if (!ok) break;
           tc_fence_after();
           const uint32_t base = kv_cnt;
-          for (int j = 0; j <= n && ok; ++j) {
-            const uint32_t ks = (base + 2 * j) % C::NS;
-            const uint32_t vs = (base + 2 * j - 1) % C::NS;  // slot of V_{j-1} (j >= 1)
-            bool v_ready = false, k_ready = false;
+          // Each sub-tile in turn: O_h += P_h V of its last tile, then S_h = Q K^T of its next one (S_h
+          // is free then: P lies over it). Both sub-tiles take every tile, or (dual) every second.
+          const int step = dual ? 2 : 1;
+          for (int t0 = 0; t0 < n + step && ok; t0 += step) {
 #pragma unroll
             for (int h = 0; h < C::SUBS; ++h) {
-              if (h >= subs) break;
-              if (j >= 1) {
-                // ---- O_h += P_h(j-1) V_{j-1}
-                if (!v_ready) {
-                  ok = mbar_wait(BAR(B_KVF + vs), ((base + 2 * j - 1) / C::NS) & 1u, abort_flag,
-                                 tmo, ecode | 5);
-                  if (!ok) break;
-                  v_ready = true;
-                }
+              const int t = t0 + (dual ? h : 0), tp = t - step;
+              const bool frees = dual || h == C::SUBS - 1;  // no other sub-tile needs the K or V
+              if (tp >= 0 && tp < n) {
+                const uint32_t vi = base + 2 * tp + 1, vs = vi % C::NS;
+                ok = mbar_wait(BAR(B_KVF + vs), (vi / C::NS) & 1u, abort_flag, tmo, ecode | 5);
+                if (!ok) break;
                 ok = mbar_wait_spin(BAR(B_PF + h), pv_cnt[h] & 1u, abort_flag, tmo, ecode | 3);
                 if (!ok) break;
-                if (j == 1) {
+                if (tp < step) {  // the sub-tile's first tile: O_h has been read
                   ok = mbar_wait(BAR(B_OE + h), (oe_cnt[h] & 1u) ^ 1u, abort_flag, tmo, ecode | 4);
                   if (!ok) break;
                   ++oe_cnt[h];
@@ -398,22 +428,19 @@ __global__ void __launch_bounds__(384, 1)
                 for (int kk = 0; kk < 8; ++kk) {
                   const uint64_t bd = umma_desc_sw128(vbase + kk * 16 * 128, C::ATOM_BYTES, 1024);
                   mma_ts(tmem + C::TM_O + h * D, tmem + h * 128 + kk * 8, bd, IDESC_PV,
-                         (j == 1 && kk == 0) ? 0u : 1u);
+                         (tp < step && kk == 0) ? 0u : 1u);
                 }
                 ++pv_cnt[h];
-                if (j == n) mma_commit(BAR(B_OF + h));
+                if (tp + step >= n) mma_commit(BAR(B_OF + h));
+                if (frees) mma_commit(BAR(B_KVE + vs));
               }
-              if (j < n) {
-                // ---- S_h = Q_h K_j^T
-                if (!k_ready) {
-                  ok = mbar_wait(BAR(B_KVF + ks), ((base + 2 * j) / C::NS) & 1u, abort_flag, tmo,
-                                 ecode | 7);
-                  if (!ok) break;
-                  tc_fence_after();
-                  k_ready = true;
-                }
+              if (t < n) {
+                const uint32_t ki = base + 2 * t, ks = ki % C::NS;
+                ok = mbar_wait(BAR(B_KVF + ks), (ki / C::NS) & 1u, abort_flag, tmo, ecode | 7);
+                if (!ok) break;
+                tc_fence_after();
                 const uint32_t kbase = kv_s0 + ks * C::TILE_BYTES;
-                const uint32_t qbase = q_s + h * C::TILE_BYTES;
+                const uint32_t qbase = q_s + (dual ? 0 : h) * C::TILE_BYTES;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                   const uint32_t off = (kk >> 2) * C::ATOM_BYTES + (kk & 3) * 32;
@@ -421,12 +448,10 @@ __global__ void __launch_bounds__(384, 1)
                          umma_desc_sw128(kbase + off, 16, 1024), IDESC_QK, kk > 0 ? 1u : 0u);
                 }
                 mma_commit(BAR(B_SF + h));
+                if (frees) mma_commit(BAR(B_KVE + ks));
+                if (frees && t == n - 1) mma_commit(BAR(B_QE));
               }
             }
-            if (!ok) break;
-            if (j >= 1) mma_commit(BAR(B_KVE + vs));
-            if (j < n) mma_commit(BAR(B_KVE + ks));
-            if (j == n - 1) mma_commit(BAR(B_QE));
           }
           if (!ok) break;
           kv_cnt = base + 2 * n;
@@ -436,6 +461,38 @@ __global__ void __launch_bounds__(384, 1)
         mma_commit(BAR(B_DR));
         volatile int never = 0;
         mbar_wait(BAR(B_DR), 0, &never, tmo, ecode | 14);
+      }
+      __syncwarp();
+    } else if (warp == 10) {
+      // -------------------------------------------------------------- scheduler
+      TreeWalk<C::ROWS> w;
+      w.init(p);
+      if (lane == 0) {
+        TreeFrag f;
+        for (uint32_t k = 0;; ++k) {
+          const uint32_t e = queue + 64u * (k % C::QD);
+          if (!mbar_wait(BAR(B_IE + k % C::QD), ((k / C::QD) & 1u) ^ 1u, abort_flag, tmo,
+                         ecode | 17))
+            break;
+          const bool more = w.next(p, f);
+          int flags = 0;
+          if (more) {
+            sts_s32(e + TQ_B, f.b);
+            sts_s32(e + TQ_G, f.g);
+            sts_s32(e + TQ_ROW0, f.row0);
+            sts_s32(e + TQ_Q0, f.q0);
+            sts_s32(e + TQ_NQ, f.nq);
+            sts_s32(e + TQ_CTX, f.ctx);
+            sts_s32(e + TQ_L, f.L);
+            sts_s32(e + TQ_T0, f.t0);
+            sts_s32(e + TQ_T1, f.t1);
+            flags = TF_LIVE | (f.dual ? TF_DUAL : 0) | (f.whole ? TF_WHOLE : 0) |
+                    (f.first ? TF_FIRST : 0);
+          }
+          sts_s32(e + TQ_FLAGS, flags);
+          mbar_arrive(BAR(B_IF + k % C::QD));
+          if (!more) break;
+        }
       }
       __syncwarp();
     }
@@ -457,75 +514,152 @@ __global__ void __launch_bounds__(384, 1)
       const bool al32 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0 && (p.dh & 15) == 0;
       FwdParams fp{};
       fp.c1 = p.c1;
-      TreeWalk<C::ROWS> w;
-      w.init(p);
-      TreeFrag f;
-      uint32_t n_frag = 0, tile = 0, ocnt = 0, kv_cnt = 0;
+      float* ml = reinterpret_cast<float*>(smem + C::SMEM_ML) + 2 * r;
+      uint32_t n_frag = 0, tile = 0, ocnt = 0, ocnt1 = 0, mcnt = 0, kv_cnt = 0;
       bool ok = true;
-      while (ok && w.next(p, f)) {
-        const int n = f.t1 - f.t0;
-        const int rho = f.row0 + h * 128 + r;
-        const bool live = rho < f.nq * p.R;
-        const int tok = live ? rho / p.R : 0;
-        const int head = f.g * p.R + (live ? rho - tok * p.R : 0);
-        const size_t orow = (static_cast<size_t>(f.q0 + tok) * p.hq + head) * p.dh;
+      // This thread's row of the range at queue entry e: token, head, whether there is one.
+      auto my_row = [&](uint32_t e, int sub, int& tok, int& head) {
+        const int rho = lds_s32(e + TQ_ROW0) + sub * 128 + r;
+        const bool live = rho < lds_s32(e + TQ_NQ) * p.R;
+        tok = live ? rho / p.R : 0;
+        head = lds_s32(e + TQ_G) * p.R + (live ? rho - tok * p.R : 0);
+        return live;
+      };
+      while (ok) {
+        const uint32_t e = queue + 64u * (n_frag % C::QD);
+        const uint32_t bar_ie = BAR(B_IE + n_frag % C::QD);
+        ok = mbar_wait(BAR(B_IF + n_frag % C::QD), (n_frag / C::QD) & 1u, abort_flag, tmo,
+                       ecode | 18);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const int flags = lds_s32(e + TQ_FLAGS);
+        if (flags == 0) break;
+        const int t1 = lds_s32(e + TQ_T1);
+        const int n = t1 - lds_s32(e + TQ_T0);
+        const int ctx = lds_s32(e + TQ_CTX);
+        const bool dual = (flags & TF_DUAL) != 0;
+        const int hq = dual ? 0 : h;  // sub-tile of this warpgroup's rows
         // ---- Q row -> shared memory (128-byte swizzle), once the previous item's Q K^T are done
         ok = mbar_wait(BAR(B_QE), (n_frag & 1u) ^ 1u, abort_flag, tmo, ecode | 2);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        {
-          const uint4* src = reinterpret_cast<const uint4*>(
-              reinterpret_cast<const OutT*>(p.q) + orow);
-          const uint32_t dst = q_s + h * C::TILE_BYTES + static_cast<uint32_t>(r) * 128u;
-          const int n16 = p.dh >> 3;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i) {
-            const uint4 v = (live && i < n16) ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
-            st_shared_v4(dst + (i >> 3) * C::ATOM_BYTES +
-                             (static_cast<uint32_t>((i & 7) ^ (r & 7)) << 4),
-                         v.x, v.y, v.z, v.w);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(BAR(B_QF));
-        }
-        ++n_frag;
-        const bool active = h == 0 || f.nq * p.R - f.row0 > 128;
-        if (!active) {
-          kv_cnt += 2 * n;
-          continue;
-        }
-        const uint32_t* mrow = p.mask + static_cast<size_t>(f.q0 + tok) * p.mask_words;
+        int qtok;  // this row's packed token (what else is needed rarely stays in the queue entry)
         float slope2 = 0.f;
         int pos = 0;
-        if constexpr (ALIBI) {
-          slope2 = __ldg(p.slopes + head) * LOG2E;
-          pos = f.ctx + tree_depth(mrow, p.mask_words, tok, f.nq);
+        {
+          int tok, head;
+          const bool live = my_row(e, hq, tok, head);
+          const int q0 = lds_s32(e + TQ_Q0);
+          qtok = q0 + tok;
+          if constexpr (ALIBI) {
+            slope2 = __ldg(p.slopes + head) * LOG2E;
+            pos = ctx + tree_depth(p.mask + static_cast<size_t>(qtok) * p.mask_words, p.mask_words,
+                                   tok, lds_s32(e + TQ_NQ));
+          }
+          if (h == hq) {
+            const uint4* src = reinterpret_cast<const uint4*>(
+                reinterpret_cast<const OutT*>(p.q) +
+                (static_cast<size_t>(qtok) * p.hq + head) * p.dh);
+            const uint32_t dst = q_s + h * C::TILE_BYTES + static_cast<uint32_t>(r) * 128u;
+            const int n16 = p.dh >> 3;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              const uint4 v = (live && i < n16) ? __ldg(src + i) : make_uint4(0u, 0u, 0u, 0u);
+              st_shared_v4(dst + (i >> 3) * C::ATOM_BYTES +
+                               (static_cast<uint32_t>((i & 7) ^ (r & 7)) << 4),
+                           v.x, v.y, v.z, v.w);
+            }
+            fence_proxy_async_smem();
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(BAR(B_QF));
+        ++n_frag;
+        const int step = dual ? 2 : 1, jj0 = dual ? h : 0;  // this warpgroup's tiles
+        if (jj0 >= n) {  // (the second warpgroup of a single tile)
+          kv_cnt += 2 * n;
+          if (lane == 0) mbar_arrive(bar_ie);
+          continue;
+        }
+        // Slots past the sequence end may hold anything (0 * NaN is NaN in P V): the first
+        // warpgroup zeroes their V rows. V cannot be replaced meanwhile, since its P V waits for this P.
+        auto zero_tail = [&](int kv0, uint32_t vi) {
+          const uint32_t vst = kv_s0 + (vi % C::NS) * C::TILE_BYTES;
+          const int L = lds_s32(e + TQ_L);
+          bool good = mbar_wait(BAR(B_KVF + vi % C::NS), (vi / C::NS) & 1u, abort_flag, tmo,
+                                ecode | 9);
+          good = __all_sync(0xffffffffu, good);
+          const int v0 = max(L - kv0, 0);
+          for (int i = r; good && i < (128 - v0) * (D / 8); i += 128) {
+            const int rr = v0 + i / (D / 8), ch = i % (D / 8);
+            st_shared_v4(vst + (ch >> 3) * C::ATOM_BYTES + rr * 128 + ((ch & 7) << 4), 0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          return good;
+        };
+        // A warp without rows only keeps the pace: no one reads its lanes of P and O. (Its own loop:
+        // a branch around the softmax below cost the warps with rows 40 %, in spilled registers.)
+        if (lds_s32(e + TQ_ROW0) + hq * 128 + wq * 32 >= lds_s32(e + TQ_NQ) * p.R) {
+          for (int jj = jj0; jj < n && ok; jj += step, ++tile) {
+            const int kv0 = (t1 - 1 - jj) * 128;
+            ok = mbar_wait(BAR(B_SF + h), tile & 1u, abort_flag, tmo, ecode | 8);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok && h == 0 && kv0 + 128 > lds_s32(e + TQ_L))
+              ok = zero_tail(kv0, kv_cnt + 2 * jj + 1);
+            __syncwarp();
+            if (ok && lane == 0) mbar_arrive(BAR(B_PF + h));
+          }
+          kv_cnt += 2 * n;
+          const bool second = dual && n > 1;
+          if (second && h == 1 && lane == 0 && ok) mbar_arrive(BAR(B_ML));
+          if (!(dual && h == 1)) {
+            // (O must not be overwritten while the other warps still read it: this warp's word counts
+            // as theirs do, and comes after the product that the word is about)
+            if (ok) ok = mbar_wait(BAR(B_OF + h), ocnt & 1u, abort_flag, tmo, ecode | 10);
+            if (ok && second)
+              ok = mbar_wait(BAR(B_OF + 1), ocnt1 & 1u, abort_flag, tmo, ecode | 11) &&
+                   mbar_wait(BAR(B_ML), mcnt & 1u, abort_flag, tmo, ecode | 12);
+            ok = __all_sync(0xffffffffu, ok);
+            if (ok) mbar_arrive(BAR(B_OE + h));
+            if (ok && second) {
+              mbar_arrive(BAR(B_OE + 1));
+              ++mcnt;
+            }
+            if (second || !dual) ++ocnt1;
+          }
+          ++ocnt;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar_ie);
+          continue;
         }
         float m_ref = -INFINITY, l = 0.f;
-        for (int jj = 0; jj < n; ++jj) {
-          const int kv0 = (f.t1 - 1 - jj) * 128;
+        for (int jj = jj0; jj < n; jj += step) {
+          const int kv0 = (t1 - 1 - jj) * 128;
           ok = mbar_wait(BAR(B_SF + h), tile & 1u, abort_flag, tmo, ecode | 8);
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           float alpha = 1.f;
           bool resc;
-          if (kv0 + 128 <= f.ctx) {
+          if (kv0 + 128 <= ctx) {
             resc = fwd_softmax_tile<BF16, ALIBI, ALIBI, false>(
                 fp, t_s, kv0, 0x3fffffff, pos, 0x3fffffff, slope2, m_ref, l, alpha);
           } else {
+            const int L = lds_s32(e + TQ_L);
+            const uint32_t* mrow = p.mask + static_cast<size_t>(qtok) * p.mask_words;
             if constexpr (ALIBI) {
               // Positions of the tile's keys: four per lane, for the whole warp.
               __syncwarp();
 #pragma unroll
               for (int u = 0; u < 4; ++u) {
                 const int t = kv0 + lane * 4 + u;
-                const int j = t - f.ctx;
+                const int j = t - ctx;
                 int kp = t;
-                if (j >= 0 && j < f.nq)
-                  kp = f.ctx + tree_depth(p.mask + static_cast<size_t>(f.q0 + j) * p.mask_words,
-                                          p.mask_words, j, f.nq);
+                if (j >= 0 && t < L)
+                  kp = ctx + tree_depth(
+                                 p.mask + static_cast<size_t>(lds_s32(e + TQ_Q0) + j) *
+                                              p.mask_words,
+                                 p.mask_words, j, L - ctx);
                 kpos[lane * 4 + u] = static_cast<float>(kp);
               }
               __syncwarp();
@@ -533,30 +667,17 @@ __global__ void __launch_bounds__(384, 1)
             uint32_t view[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              view[u] = tree_view(mrow, p.mask_words, kv0 + u * 32, f.ctx, f.L);
+              view[u] = tree_view(mrow, p.mask_words, kv0 + u * 32, ctx, L);
             resc = tree_masked_tile<BF16, ALIBI>(p.c1, t_s, view, static_cast<float>(pos), slope2,
                                                  kpos, m_ref, l, alpha);
-            if (h == 0 && kv0 + 128 > f.L) {
-              // Slots past the sequence end may hold anything (0 * NaN is NaN in P V): zero their V
-              // rows. V cannot be replaced meanwhile, since its P V waits for this P.
-              const uint32_t vi = kv_cnt + 2 * jj + 1;
-              const uint32_t vst = kv_s0 + (vi % C::NS) * C::TILE_BYTES;
-              ok = mbar_wait(BAR(B_KVF + vi % C::NS), (vi / C::NS) & 1u, abort_flag, tmo,
-                             ecode | 9);
-              ok = __all_sync(0xffffffffu, ok);
+            if (h == 0 && kv0 + 128 > L) {
+              ok = zero_tail(kv0, kv_cnt + 2 * jj + 1);
               if (!ok) break;
-              const int v0 = max(f.L - kv0, 0);
-              for (int i = r; i < (128 - v0) * (D / 8); i += 128) {
-                const int rr = v0 + i / (D / 8), ch = i % (D / 8);
-                st_shared_v4(vst + (ch >> 3) * C::ATOM_BYTES + rr * 128 + ((ch & 7) << 4), 0, 0, 0,
-                             0);
-              }
-              fence_proxy_async_smem();
             }
           }
           // O_h holds the tiles visited before this one, and its last P V has completed (it was
           // issued before this Q K^T).
-          if (jj > 0 && __any_sync(0xffffffffu, resc)) {
+          if (jj > jj0 && __any_sync(0xffffffffu, resc)) {
 #pragma unroll 1
             for (int c4 = 0; c4 < D / 32; ++c4) {
               uint32_t o[32];
@@ -576,37 +697,84 @@ __global__ void __launch_bounds__(384, 1)
         if (!ok) break;
         kv_cnt += 2 * n;
         // ---- epilogue: O / l and the log-sum-exp, to the outputs or to the partials
+        if (dual && h == 1) {  // the first warpgroup has the rest
+          ml[0] = m_ref;
+          ml[1] = l;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(BAR(B_ML));
+            mbar_arrive(bar_ie);
+          }
+          ++ocnt;  // (the first warpgroup waits for this O)
+          continue;
+        }
         ok = mbar_wait(BAR(B_OF + h), ocnt & 1u, abort_flag, tmo, ecode | 10);
+        const bool joined = dual && n > 1;
+        if (joined) {
+          if (ok) ok = mbar_wait(BAR(B_OF + 1), ocnt1 & 1u, abort_flag, tmo, ecode | 11);
+          if (ok) ok = mbar_wait(BAR(B_ML), mcnt & 1u, abort_flag, tmo, ecode | 12);
+        }
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         ++ocnt;
+        if (joined || !dual) ++ocnt1;  // phases of the second O's barrier
         tc_fence_after();
+        // Weights of this warpgroup's O and, where joined, of the second's.
+        float s0 = 1.f, s1 = 0.f;
+        if (joined) {
+          ++mcnt;
+          const float m1 = ml[0], l1 = ml[1];
+          const float m = fmaxf(m_ref, m1);
+          s0 = m == -INFINITY ? 0.f : ex2_approx(m_ref - m);
+          s1 = m == -INFINITY ? 0.f : ex2_approx(m1 - m);
+          l = l * s0 + l1 * s1;
+          m_ref = m;
+        }
         const float inv_l = l > 0.f ? 1.f / l : 0.f;
         const float lse2 = l > 0.f ? m_ref + __log2f(l) : -INFINITY;
-        const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (f.first ? 0 : 1)) * C::ROWS +
-                            h * 128 + r;
+        s0 *= inv_l;
+        s1 *= inv_l;
+        int tok, head;
+        const bool live = my_row(e, hq, tok, head);
+        const bool whole = (flags & TF_WHOLE) != 0;
+        const int q0 = lds_s32(e + TQ_Q0);
+        const size_t orow = (static_cast<size_t>(q0 + tok) * p.hq + head) * p.dh;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar_ie);  // the entry has been read
+        const size_t slot = (2 * static_cast<size_t>(blockIdx.x) + (flags & TF_FIRST ? 0 : 1)) *
+                                C::ROWS + hq * 128 + r;
         if (live) {
-          if (!f.whole)
+          if (!whole)
             p.ws_lse[slot] = lse2;
           else if (p.lse)
-            p.lse[static_cast<size_t>(head) * p.total_q + f.q0 + tok] = lse2 * LN2;
+            p.lse[static_cast<size_t>(head) * p.total_q + q0 + tok] = lse2 * LN2;
         }
 #pragma unroll
         for (int c4 = 0; c4 < D / 32; ++c4) {
           uint32_t o[32];
+          uint32_t o1[32];
           tmem_ld32(t_o + c4 * 32, o);
+          if (joined) tmem_ld32(t_o + D + c4 * 32, o1);
           tmem_wait_ld();
           if (c4 == D / 32 - 1) {
-            // O_h has been read: it is free for the next item's P V.
+            // O has been read: it is free for the next item's P V.
             tc_fence_before();
             mbar_arrive(BAR(B_OE + h));
+            if (joined) mbar_arrive(BAR(B_OE + 1));
           }
           if (!live) continue;
-          if (f.whole) {
+          if (joined) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              o[i] = __float_as_uint(__uint_as_float(o[i]) * s0 + __uint_as_float(o1[i]) * s1);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * s0);
+          }
+          if (whole) {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              o[i] = pack2<BF16>(__uint_as_float(o[2 * i]) * inv_l,
-                                 __uint_as_float(o[2 * i + 1]) * inv_l);
+              o[i] = pack2<BF16>(__uint_as_float(o[2 * i]), __uint_as_float(o[2 * i + 1]));
             OutT* dst = reinterpret_cast<OutT*>(p.out) + orow + c4 * 32;
             const int left = p.dh - c4 * 32;  // columns of this piece that exist
             if (al32) {
@@ -620,9 +788,6 @@ __global__ void __launch_bounds__(384, 1)
                       make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
             }
           } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              o[i] = __float_as_uint(__uint_as_float(o[i]) * inv_l);
             float* dst = p.ws_o + slot * D + c4 * 32;
 #pragma unroll
             for (int i = 0; i < 4; ++i) st_global_v8(dst + 8 * i, &o[8 * i]);

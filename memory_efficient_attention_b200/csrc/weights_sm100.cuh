@@ -21,12 +21,14 @@
 // result is deterministic.
 //
 // Roles: warp 16 the tcgen05 issuer, warp 17 the TMA producer, warp 18 the columns' terms (log-sum-exp
-// and ALiBi), warpgroups 0-3 the sums: warpgroup w takes key tile w % SUBS and part w / SUBS of the
-// columns.
+// and ALiBi), warpgroups 0-3 the sums: warpgroup w takes key tile w % SUBS of every NBUF-th step (a
+// step costs a warp about 100 instructions beside its columns', so half tiles of every step are
+// slower).
 //
 // Bound by the exponentials: a score costs 2 D flop on the tensor cores and one exp2, and an SM does
-// 16 exp2 a clock: 1024 clocks for a 128 x 128 tile, whose product takes 512 at D = 128. Six of sixteen
-// column pairs therefore take a degree-4 polynomial on the FMA pipes instead (see exp2_poly2).
+// 16 exp2 a clock: 1024 clocks for a 128 x 128 tile, whose product takes 512 at D = 128. (A quarter to
+// three eighths of them by a polynomial on the FMA pipes took fewer clocks and as much time or more:
+// the card is at its power limit here, and the longer instruction stream lowers the clock.)
 #pragma once
 
 #include <cuda_bf16.h>
@@ -54,23 +56,25 @@ template <int D>
 struct WeightsCfg {
   static constexpr int SUBS = D == 256 ? 1 : 2;  // 128-key tiles per item
   static constexpr int KT = 128 * SUBS;
-  static constexpr int PARTS = 4 / SUBS;         // column parts, one per warpgroup of a key tile
-  static constexpr int COLS = 128 / PARTS;
-  static constexpr int NBUF = 4 / SUBS;          // S buffers (512 TMEM columns in all)
+  static constexpr int NBUF = 4 / SUBS;          // S buffers (512 TMEM columns), one per step
   static constexpr int ATOMS = D / 64;
   static constexpr uint32_t ATOM_BYTES = 128 * 128;
   static constexpr uint32_t TILE_BYTES = 128 * D * 2;
   static constexpr int NK = D == 256 ? 1 : 2;    // items whose K is in shared memory
   static constexpr int NQ = D == 64 ? 4 : 2;     // Q tiles in the ring
-  static constexpr int NT = 4;                   // steps whose column terms are in shared memory
   static constexpr uint32_t SMEM_K = 0;
   static constexpr uint32_t SMEM_Q = NK * SUBS * TILE_BYTES;
-  static constexpr uint32_t SMEM_T = SMEM_Q + NQ * TILE_BYTES;   // NT x 3 x 128 floats
-  static constexpr uint32_t SMEM_SUM = SMEM_T + NT * 3 * 512;    // 3 warpgroups x 128 floats
+  static constexpr uint32_t SMEM_T = SMEM_Q + NQ * TILE_BYTES;   // 2 NBUF x 3 x 128 floats
+  static constexpr uint32_t SMEM_SUM = SMEM_T + 2 * NBUF * 3 * 512;  // 3 warpgroups x 128 floats
   static constexpr uint32_t SMEM_MISC = SMEM_SUM + 3 * 512;
   static constexpr uint32_t SMEM_TOTAL = SMEM_MISC + 256 + 1024;
   static_assert(SMEM_TOTAL <= 232448, "shared memory per CTA");
   static constexpr int THREADS = 640;
+  // Launched at 96 registers a thread (640 x 96 = 61440): the warps beside the sums give theirs down
+  // to REGS_OTHER, and 512 * REGS_SUM + 128 * REGS_OTHER must not exceed 61440.
+  static constexpr int REGS_SUM = 104;
+  static constexpr int REGS_OTHER = 64;
+  static_assert(512 * REGS_SUM + 128 * REGS_OTHER <= 640 * 96, "register split");
 };
 
 // A CTA's range of one item's steps.
@@ -81,19 +85,22 @@ struct WeightsFrag {
   bool whole, first;
 };
 
+// A segment's items: items before n0 have queries [qw, lq) and nt0 Q tiles; under a causal mask those
+// from n0 on start at their first key's own query, and have a - kt * (KT / QT) Q tiles (KT is a
+// multiple of a Q tile's QT queries, so the tile counts fall in equal steps).
 struct WeightsSeq {
-  int q0, lq, k0, lk, items;
+  int q0, lq, k0, lk, items, n0, nt0, a, qw;
   long long work;  // steps of the segment's items of one KV head
 };
 
-template <int KT, bool CAUSAL>
-__device__ __forceinline__ void weights_item(const WeightsParams& p, const WeightsSeq& s, int kt,
-                                             int& qbeg, int& nt) {
-  qbeg = p.last > 0 ? max(s.lq - p.last, 0) : 0;
-  if (CAUSAL) qbeg = max(qbeg, kt * KT - (s.lk - s.lq));  // the first query that sees its first key
-  const int qt = 128 >> p.log2_p;
-  // (an item that no query sees still has a step, which finds nothing, so that zeros are written)
-  nt = qbeg < s.lq ? (s.lq - qbeg + qt - 1) / qt : 1;
+// Steps per head block before item kt.
+template <int KT>
+__device__ __forceinline__ long long weights_before(const WeightsParams& p, const WeightsSeq& s,
+                                                    int kt) {
+  if (kt <= s.n0) return static_cast<long long>(kt) * s.nt0;
+  const int drop = KT >> (7 - p.log2_p);  // KT / QT
+  const long long m = kt - s.n0;
+  return static_cast<long long>(s.n0) * s.nt0 + m * s.a - drop * ((s.n0 + kt - 1) * m / 2);
 }
 
 template <int KT, bool CAUSAL>
@@ -104,12 +111,17 @@ __device__ __forceinline__ WeightsSeq weights_seq(const WeightsParams& p, int se
   s.k0 = __ldg(p.cu_k + seg);
   s.lk = max(__ldg(p.cu_k + seg + 1) - s.k0, 0);
   s.items = (s.lk + KT - 1) / KT;
-  s.work = 0;
-  for (int kt = 0; kt < s.items; ++kt) {
-    int qbeg, nt;
-    weights_item<KT, CAUSAL>(p, s, kt, qbeg, nt);
-    s.work += static_cast<long long>(nt) * (p.R >> p.log2_p);
+  const int lqt = 7 - p.log2_p, qt1 = (1 << lqt) - 1;
+  s.qw = p.last > 0 ? max(s.lq - p.last, 0) : 0;
+  // (an item that no query sees still has a step, which finds nothing, so that zeros are written)
+  s.nt0 = max((s.lq - s.qw + qt1) >> lqt, 1);
+  s.a = (s.lk + qt1) >> lqt;
+  s.n0 = s.items;
+  if (CAUSAL) {
+    const int first = s.qw + s.lk - s.lq;  // key position of the first query that counts
+    s.n0 = first < 0 ? 0 : min(first / KT + 1, s.items);
   }
+  s.work = weights_before<KT>(p, s, s.items) * (p.R >> p.log2_p);
   return s;
 }
 
@@ -158,7 +170,8 @@ struct WeightsWalk {
   int seg, g, kt, qbeg, nt, len;    // len: steps of the item
   WeightsSeq s;
   __device__ __forceinline__ void load_item(const WeightsParams& p) {
-    weights_item<KT, CAUSAL>(p, s, kt, qbeg, nt);
+    nt = kt < s.n0 ? s.nt0 : s.a - kt * (KT >> (7 - p.log2_p));
+    qbeg = kt < s.n0 ? s.qw : kt * KT - (s.lk - s.lq);
     len = nt * (p.R >> p.log2_p);
   }
   // Moves to the item that holds step `pos` (at or after the current one).
@@ -190,9 +203,19 @@ struct WeightsWalk {
     s = weights_seq<KT, CAUSAL>(p, seg);
     g = static_cast<int>((at - base) / s.work);
     base += s.work * g;
-    kt = 0;
+    // The last item that starts at or before `at`.
+    const int hbn = p.R >> p.log2_p;
+    int lo = 0, hi = s.items - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (weights_before<KT>(p, s, mid) * hbn <= at - base)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    kt = lo;
+    base += weights_before<KT>(p, s, kt) * hbn;
     load_item(p);
-    advance(p);
   }
   __device__ __forceinline__ bool next(const WeightsParams& p, WeightsFrag& f) {
     if (pos >= end) return false;
@@ -215,62 +238,29 @@ struct WeightsWalk {
   }
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
-// 2^e for a pair of values of at most about 100, on the FMA and integer pipes: e = n + f with n the nearest
-// integer (added as 1.5 * 2^23, which leaves n in the low mantissa bits), 2^f by the degree-4
-// polynomial of least relative error on [-1/2, 1/2] (2.7e-6 in fp32, 4e-8 on average), n added to
-// the exponent. Values below -126 give about 2^-126.
-__device__ __forceinline__ uint64_t exp2_poly2(uint64_t e) {
-  float e0, e1;
-  f2_unpack(e, e0, e1);
-  // (a NaN stays one up to here and comes out as a huge value, not as a weight)
-  e = f2_pack(max_nan(e0, -126.f), max_nan(e1, -126.f));
-  const uint64_t magic = f2_pack(12582912.f, 12582912.f);
-  const uint64_t z = f2_add(e, magic);
-  const uint64_t n = f2_add(z, f2_pack(-12582912.f, -12582912.f));
-  const uint64_t f = f2_fma(n, f2_pack(-1.f, -1.f), e);
-  uint64_t r = f2_pack(0.009570102207362652f, 0.009570102207362652f);
-  r = f2_fma(r, f, f2_pack(0.05591785907745361f, 0.05591785907745361f));
-  r = f2_fma(r, f, f2_pack(0.240247443318367f, 0.240247443318367f));
-  r = f2_fma(r, f, f2_pack(0.6931217908859253f, 0.6931217908859253f));
-  r = f2_fma(r, f, f2_pack(0.9999992847442627f, 0.9999992847442627f));
-  float r0, r1, z0, z1;
-  f2_unpack(r, r0, r1);
-  f2_unpack(z, z0, z1);
-  return f2_pack(__int_as_float(__float_as_int(r0) + (__float_as_int(z0) << 23)),
-                 __int_as_float(__float_as_int(r1) + (__float_as_int(z1) << 23)));
-}
-
-// Column pairs of 16 that take the polynomial.
-constexpr uint32_t kWeightsPoly = 0x4A52u;
-
 // Adds 2^score over 32 columns of one key to acc. x: the raw products; terms: shared memory, this
 // chunk's row terms (nl, and with ALiBi the slopes and, non-causal, the queries' positions); key: the
-// key's index in the item. EDGE: only columns [lo, hi) of the chunk count.
+// key's index in the item. EDGE: only the columns whose bit of `live` is set count.
 template <bool CAUSAL, bool ALIBI, bool EDGE>
-__device__ __forceinline__ void weights_chunk(const uint32_t (&x)[32], uint32_t terms,
-                                              uint64_t c1x2, float key, int lo, int hi,
+__device__ __forceinline__ void weights_chunk(const uint32_t (&x)[32], const float* terms,
+                                              uint64_t c1x2, float key, uint32_t live,
                                               uint64_t (&acc)[4]) {
   const uint64_t keyx2 = f2_pack(key, key);
 #pragma unroll
   for (int i = 0; i < 32; i += 4) {
-    uint64_t nl[2], sl[2] = {0ull, 0ull}, ps[2] = {0ull, 0ull};
-    asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
-                 : "=l"(nl[0]), "=l"(nl[1])
-                 : "r"(terms + i * 4));
-    if constexpr (ALIBI)
-      asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
-                   : "=l"(sl[0]), "=l"(sl[1])
-                   : "r"(terms + 512 + i * 4));
-    if constexpr (ALIBI && !CAUSAL)
-      asm volatile("ld.shared.v2.b64 {%0, %1}, [%2];"
-                   : "=l"(ps[0]), "=l"(ps[1])
-                   : "r"(terms + 1024 + i * 4));
+    const ulonglong2 nl2 = *reinterpret_cast<const ulonglong2*>(terms + i);
+    const uint64_t nl[2] = {nl2.x, nl2.y};
+    uint64_t sl[2] = {0ull, 0ull}, ps[2] = {0ull, 0ull};
+    if constexpr (ALIBI) {
+      const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(terms + 128 + i);
+      sl[0] = v.x;
+      sl[1] = v.y;
+    }
+    if constexpr (ALIBI && !CAUSAL) {
+      const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(terms + 256 + i);
+      ps[0] = v.x;
+      ps[1] = v.y;
+    }
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
       const int c = i + 2 * u;
@@ -281,22 +271,23 @@ __device__ __forceinline__ void weights_chunk(const uint32_t (&x)[32], uint32_t 
         f2_unpack(ps[u], p0, p1);
         e = f2_fma(sl[u], f2_pack(-fabsf(p0 - key), -fabsf(p1 - key)), e);
       }
-      uint64_t w;
-      if ((kWeightsPoly >> (c >> 1)) & 1u) {
-        w = exp2_poly2(e);
-      } else {
-        float e0, e1;
-        f2_unpack(e, e0, e1);
-        w = f2_pack(ex2_approx(e0), ex2_approx(e1));
-      }
+      float w0, w1;
+      f2_unpack(e, w0, w1);
+      w0 = ex2_approx(w0);
+      w1 = ex2_approx(w1);
       if constexpr (EDGE) {  // (a column that does not count may hold anything)
-        float w0, w1;
-        f2_unpack(w, w0, w1);
-        w = f2_pack(c >= lo && c < hi ? w0 : 0.f, c + 1 >= lo && c + 1 < hi ? w1 : 0.f);
+        w0 = (live >> c) & 1u ? w0 : 0.f;
+        w1 = (live >> (c + 1)) & 1u ? w1 : 0.f;
       }
-      acc[(i >> 1 & 2) + u] = f2_add(acc[(i >> 1 & 2) + u], w);
+      acc[(i >> 1 & 2) + u] = f2_add(acc[(i >> 1 & 2) + u], f2_pack(w0, w1));
     }
   }
+}
+
+// Bits [lo, hi) of a chunk of 32 (either end may lie outside it).
+__device__ __forceinline__ uint32_t weights_live(int lo, int hi) {
+  const uint32_t below = hi >= 32 ? 0xFFFFFFFFu : hi <= 0 ? 0u : (1u << hi) - 1u;
+  return lo >= 32 ? 0u : lo <= 0 ? below : below & (0xFFFFFFFFu << lo);
 }
 
 template <int D, bool BF16, bool CAUSAL, bool ALIBI>
@@ -311,8 +302,8 @@ __global__ void __launch_bounds__(640, 1)
   uint8_t* smem = smem_raw + pad;
   const uint32_t sbase = smem_u32(smem);
   constexpr int B_KF = 0, B_KE = B_KF + C::NK, B_QF = B_KE + C::NK, B_QE = B_QF + C::NQ;
-  constexpr int B_SF = B_QE + C::NQ, B_SE = B_SF + C::NBUF, B_TF = B_SE + C::NBUF;
-  constexpr int B_TE = B_TF + C::NT, B_CF = B_TE + C::NT, B_CE = B_CF + 1, B_DR = B_CE + 1;
+  constexpr int B_SF = B_QE + C::NQ, B_SE = B_SF + 4, B_CF = B_SE + 4;  // S: per (buffer, tile)
+  constexpr int B_CE = B_CF + 1, B_DR = B_CE + 1;
   constexpr int N_BARS = B_DR + 1;
   static_assert(8 * N_BARS + 8 <= 256, "barrier region");
   const uint32_t bar0 = sbase + C::SMEM_MISC;
@@ -332,16 +323,12 @@ __global__ void __launch_bounds__(640, 1)
       mbar_init(BAR(B_QF + s), 1);
       mbar_init(BAR(B_QE + s), 1);
     }
-    for (int s = 0; s < C::NBUF; ++s) {
-      mbar_init(BAR(B_SF + s), 1);
-      mbar_init(BAR(B_SE + s), 16);  // one elected arrival per warp
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(BAR(B_SF + s), 2);  // the step's products, and its column terms
+      mbar_init(BAR(B_SE + s), 4);  // one elected arrival per warp that reads the buffer
     }
-    for (int s = 0; s < C::NT; ++s) {
-      mbar_init(BAR(B_TF + s), 1);
-      mbar_init(BAR(B_TE + s), 16);
-    }
-    mbar_init(BAR(B_CF), 4 * (4 - C::SUBS));  // warps of the parts after the first
-    mbar_init(BAR(B_CE), 4 * C::SUBS);        // warps of the first part
+    mbar_init(BAR(B_CF), 4 * (4 - C::SUBS));  // warps of the buffers after the first
+    mbar_init(BAR(B_CE), 4 * C::SUBS);        // warps of the first buffer
     mbar_init(BAR(B_DR), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -357,6 +344,10 @@ __global__ void __launch_bounds__(640, 1)
   bool ok = true;
   pdl_trigger();
 
+  if (warp >= 16)
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
+  else
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SUM));
   if (warp == 17) {
     // ---------------------------------------------------------------- TMA producer
     Walk w;
@@ -424,13 +415,13 @@ __global__ void __launch_bounds__(640, 1)
           const uint32_t s = k % C::NQ, b = k % C::NBUF;
           ok = mbar_wait(BAR(B_QF + s), (k / C::NQ) & 1u, abort_flag, tmo, ecode | 4);
           if (!ok) break;
-          ok = mbar_wait_spin(BAR(B_SE + b), ((k / C::NBUF) & 1u) ^ 1u, abort_flag, tmo,
-                              ecode | 5);
-          if (!ok) break;
-          tc_fence_after();
           const uint32_t qb = sbase + C::SMEM_Q + s * C::TILE_BYTES;
 #pragma unroll
           for (int h = 0; h < C::SUBS; ++h) {
+            ok = mbar_wait_spin(BAR(B_SE + b * C::SUBS + h), ((k / C::NBUF) & 1u) ^ 1u, abort_flag,
+                                tmo, ecode | 5);
+            if (!ok) break;
+            tc_fence_after();
             const uint32_t kbase = sbase + C::SMEM_K + (kb * C::SUBS + h) * C::TILE_BYTES;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -438,8 +429,9 @@ __global__ void __launch_bounds__(640, 1)
               mma_ss(tmem + (b * C::SUBS + h) * 128, umma_desc_sw128(kbase + o, 16, 1024),
                      umma_desc_sw128(qb + o, 16, 1024), IDESC, kk > 0 ? 1u : 0u);
             }
+            mma_commit(BAR(B_SF + b * C::SUBS + h));
           }
-          mma_commit(BAR(B_SF + b));
+          if (!ok) break;
           mma_commit(BAR(B_QE + s));
           if (st == f.s1 - 1) mma_commit(BAR(B_KE + kb));
         }
@@ -461,7 +453,7 @@ __global__ void __launch_bounds__(640, 1)
     while (ok && w.next(p, f)) {
       int hb = f.s0 / f.nt, t = f.s0 - hb * f.nt;
       for (int st = f.s0; st < f.s1; ++st, ++k) {
-        const uint32_t s = k % C::NT;
+        const uint32_t b = k % C::NBUF;
         float nl[4], sl[4], ps[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
@@ -480,10 +472,13 @@ __global__ void __launch_bounds__(640, 1)
             }
           }
         }
-        ok = mbar_wait(BAR(B_TE + s), ((k / C::NT) & 1u) ^ 1u, abort_flag, tmo, ecode | 6);
+        if (lane < C::SUBS)
+          ok = mbar_wait(BAR(B_SE + b * C::SUBS + lane), ((k / C::NBUF) & 1u) ^ 1u, abort_flag, tmo,
+                         ecode | 6);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        float* dst = reinterpret_cast<float*>(smem + C::SMEM_T) + s * 384 + lane;
+        float* dst =
+            reinterpret_cast<float*>(smem + C::SMEM_T) + (k % (2 * C::NBUF)) * 384 + lane;
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           dst[u * 32] = nl[u];
@@ -491,7 +486,7 @@ __global__ void __launch_bounds__(640, 1)
           if constexpr (ALIBI && !CAUSAL) dst[256 + u * 32] = ps[u];
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_TF + s));
+        if (lane < C::SUBS) mbar_arrive(BAR(B_SF + b * C::SUBS + lane));
         if (++t == f.nt) {
           t = 0;
           ++hb;
@@ -501,56 +496,72 @@ __global__ void __launch_bounds__(640, 1)
   } else if (warp < 16) {
     // ---------------------------------------------------------------- sums (thread = key)
     const int wg = warp >> 2;
-    const int h = wg % C::SUBS, part = wg / C::SUBS;
+    const int h = wg % C::SUBS, buf = wg / C::SUBS;
     const int r = threadIdx.x & 127;
-    const uint32_t t_lane =
-        tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + h * 128 + part * C::COLS;
+    const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) +
+                         (buf * C::SUBS + h) * 128;
+    // This warpgroup's column terms: two slots per buffer, in turn.
+    const float* terms0 = reinterpret_cast<const float*>(smem + C::SMEM_T) + buf * 384;
+    int slot = 0;
+    const uint32_t bar_f = BAR(B_SF + wg), bar_e = BAR(B_SE + wg);  // (wg = buf * SUBS + h)
     const uint64_t c1x2 = f2_pack(p.c1, p.c1);
     const float key = static_cast<float>(h * 128 + r);
     float* sums = reinterpret_cast<float*>(smem + C::SMEM_SUM);
     Walk w;
     w.init(p, gridDim.x, blockIdx.x);
     WeightsFrag f;
-    uint32_t n_frag = 0, k = 0;
+    uint32_t n_frag = 0, phase = 0;
+    int ahead = buf;  // steps until this warpgroup's next one
     while (ok && w.next(p, f)) {
       float sum = 0.f, comp = 0.f;  // running sum and what it lost
-      const int off = f.lk - f.lq;
-      const int j = f.j0 + h * 128;  // first key of this warpgroup's tile
-      int t = f.s0 % f.nt;
-      for (int st = f.s0; st < f.s1; ++st, ++k) {
-        const int qi = f.qbeg + t * (128 >> p.log2_p);  // first query of the tile
-        if (++t == f.nt) t = 0;
+      const int j = f.j0 + h * 128 - (f.lk - f.lq) - f.qbeg;  // first key, counted in queries
+      const int left = f.lq - f.qbeg;
+      int t = (f.s0 + ahead) % f.nt;
+      int n = f.s1 - f.s0 - ahead;
+      for (; n > 0; n -= C::NBUF) {
+        const int qi = t << (7 - p.log2_p);  // first query of the tile
+        t += C::NBUF;
+        while (t >= f.nt) t -= f.nt;
         // Columns [lo, hi) count for this key; every key of the tile sees all 128 off the edges.
-        const int hi = min((f.lq - qi) << p.log2_p, 128);
-        const int lo = CAUSAL ? max(j + r - off - qi, 0) << p.log2_p : 0;
-        const bool edge = hi < 128 || (CAUSAL && qi + off < j + 127);
-        const uint32_t b = k % C::NBUF, s = k % C::NT;
-        ok = mbar_wait(BAR(B_TF + s), (k / C::NT) & 1u, abort_flag, tmo, ecode | 7);
-        if (ok) ok = mbar_wait(BAR(B_SF + b), (k / C::NBUF) & 1u, abort_flag, tmo, ecode | 8);
+        const int hi = (left - qi) << p.log2_p;
+        const bool edge = hi < 128 || (CAUSAL && qi < j + 127);
+        ok = mbar_wait(bar_f, phase, abort_flag, tmo, ecode | 8);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
+        phase ^= 1u;
+        const float* terms = terms0 + slot;
+        slot = C::NBUF * 384 - slot;
         tc_fence_after();
-        const uint32_t t_s = t_lane + b * (C::SUBS * 128);
-        const uint32_t terms = sbase + C::SMEM_T + s * 1536u + part * (C::COLS * 4u);
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
-        uint32_t x[2][32];
-        tmem_ld32(t_s, x[0]);
-#pragma unroll
-        for (int c = 0; c < C::COLS / 32; ++c) {
+        // 32 columns at a time; once the last ones are in registers the buffer is free, and the next
+        // product runs under their exponentials.
+        auto load = [&](int c, uint32_t (&x)[32]) {
+          tmem_ld32(t_s + c, x);
           tmem_wait_ld();
-          if (c + 1 < C::COLS / 32) tmem_ld32(t_s + (c + 1) * 32, x[(c + 1) & 1]);
-          const int c0 = part * C::COLS + c * 32;
-          if (!edge)
-            weights_chunk<CAUSAL, ALIBI, false>(x[c & 1], terms + c * 128, c1x2, key, 0, 32, acc);
-          else if (c0 < hi)
-            weights_chunk<CAUSAL, ALIBI, true>(x[c & 1], terms + c * 128, c1x2, key, lo - c0,
-                                               hi - c0, acc);
-        }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(BAR(B_SE + b));
-          mbar_arrive(BAR(B_TE + s));
+          if (c == 96) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar_e);
+          }
+        };
+        if (!edge) {
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t x[32];
+            load(c, x);
+            weights_chunk<CAUSAL, ALIBI, false>(x, terms + c, c1x2, key, 0u, acc);
+          }
+        } else {
+          const int lo = CAUSAL ? max(j + r - qi, 0) << p.log2_p : 0;
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 32) {
+            uint32_t x[32];
+            load(c, x);
+            const uint32_t live = weights_live(lo - c, hi - c);
+            // (columns that no key of the warp counts are left out)
+            if (__any_sync(0xffffffffu, live != 0u))
+              weights_chunk<CAUSAL, ALIBI, true>(x, terms + c, c1x2, key, live, acc);
+          }
         }
         float a0, a1;
         f2_unpack(f2_add(f2_add(acc[0], acc[1]), f2_add(acc[2], acc[3])), a0, a1);
@@ -560,9 +571,10 @@ __global__ void __launch_bounds__(640, 1)
         comp = (s2 - sum) - y;
         sum = s2;
       }
+      ahead = -n;
       if (!ok) break;
-      // ---- the parts join, and the item's (or the range's) sums are written
-      if (part > 0) {
+      // ---- the warpgroups' sums join, and the item's (or the range's) are written
+      if (buf > 0) {
         ok = mbar_wait(BAR(B_CE), (n_frag & 1u) ^ 1u, abort_flag, tmo, ecode | 9);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
@@ -574,7 +586,7 @@ __global__ void __launch_bounds__(640, 1)
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
 #pragma unroll
-        for (int q = 1; q < C::PARTS; ++q) sum += sums[(q * C::SUBS + h - C::SUBS) * 128 + r];
+        for (int q = 1; q < C::NBUF; ++q) sum += sums[(q * C::SUBS + h - C::SUBS) * 128 + r];
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_CE));
         const int row = h * 128 + r;

@@ -312,6 +312,8 @@ def random_tree(n, gen):
     ([385, 191], [12, 30], 4, 1, 256, FP, 192, True),
     ([5000], [17], 64, 8, 128, BF, 16, False),                   # one request over many CTAs
     ([256] * 70, [4] * 70, 8, 2, 40, FP, 64, True),
+    ([3000, 1700, 129, 128], [16, 2, 1, 16], 16, 2, 128, BF, 16, True),  # one sub-tile's rows
+    ([4000, 300] * 30, [40, 3] * 30, 16, 2, 64, FP, 32, False),  # one and two sub-tiles in turn
 ])
 def test_tree(lens, nq, hq, hkv, d, dtype, bs, alibi):
     c = ref.Cache(lens, hq, hkv, d, dtype, bs, 81)
