@@ -402,6 +402,23 @@ int mea_decode_tree(const void* q, const void* k_cache, const void* v_cache,
                     int n_heads_kv, int head_dim, float scale, const float* alibi_slopes,
                     int dtype, void* workspace, size_t workspace_bytes, void* stream);
 
+/*
+ * mea_call — one of the calls above with its arguments, in their order, in an array of 8-byte words:
+ * integers as int64, pointers as addresses (0 for NULL), the scale as a double. For bindings that pay
+ * for every argument: the checks, the launches and the result are those of the call itself. Returns
+ * MEA_ERR_SHAPE for an unknown entry, MEA_ERR_NULL without words.
+ */
+typedef enum {
+  MEA_CALL_BLOCK_KEY_BOUNDS = 1,
+  MEA_CALL_SELECT_BLOCKS = 2,
+  MEA_CALL_DECODE_SELECTED = 3,
+  MEA_CALL_DECODE_WEIGHTS = 4,
+  MEA_CALL_ATTENTION_WEIGHTS = 5,
+  MEA_CALL_EVICT_PAGED = 6,
+  MEA_CALL_DECODE_TREE = 7
+} mea_call_entry;
+int mea_call(int entry, const void* words);
+
 /* mea_status_string — a static English description of a mea_status value. */
 const char* mea_status_string(int status);
 

@@ -515,16 +515,22 @@ def _check_weights(name: str, t: torch.Tensor, n: int, hkv: int, max_k: int, idx
 
 
 def _launch(idx: int, name: str, *args) -> None:
-    """Calls library function ``name`` with GPU ``idx`` current and its current stream as the last
-    argument (a launch goes to the current device, whichever the tensors live on)."""
-    fn = getattr(_lib.load(), name)
+    """Calls library function ``name`` (through mea_call: one block of words costs a fraction of two
+    dozen ctypes arguments) with GPU ``idx`` current and its current stream as the last argument (a
+    launch goes to the current device, whichever the tensors live on)."""
+    entry, words = _lib.CALLS[name]
+    call = _lib.load().mea_call
     if _cur_device() == idx:
-        rc = fn(*args, _raw_stream(idx))
+        rc = call(entry, words.pack(*args, _raw_stream(idx)))
     else:
         with torch.cuda.device(idx):
-            rc = fn(*args, _raw_stream(idx))
+            rc = call(entry, words.pack(*args, _raw_stream(idx)))
     if rc != _lib.MEA_OK:
         raise MeaError(rc, name)
+
+
+def _addr(t: Optional[torch.Tensor]) -> int:
+    return 0 if t is None else t.data_ptr()
 
 
 def block_key_bounds(k_cache: torch.Tensor, block_table: torch.Tensor,
@@ -547,7 +553,7 @@ def block_key_bounds(k_cache: torch.Tensor, block_table: torch.Tensor,
     else:
         _output("bounds", bounds, (nb, hkv, 2, d), k_cache.dtype, idx)
     _launch(idx, "mea_block_key_bounds", k_cache.data_ptr(), table.data_ptr(), cu.data_ptr(),
-            _ptr(first), bounds.data_ptr(), n, nb, bs, max_blocks, int(max_seqlen_k), hkv, d, code)
+            _addr(first), bounds.data_ptr(), n, nb, bs, max_blocks, int(max_seqlen_k), hkv, d, code)
     return bounds
 
 
@@ -617,7 +623,7 @@ def decode_paged_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     slopes = _slopes_for(alibi_slopes, hq, idx)
     _launch(idx, "mea_decode_selected", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             table.data_ptr(), cu.data_ptr(), selected.data_ptr(), out.data_ptr(), lse.data_ptr(),
-            n, nb, bs, table.size(1), n_select, hq, hkv, d, _scale_for(scale, d), _ptr(slopes),
+            n, nb, bs, table.size(1), n_select, hq, hkv, d, _scale_for(scale, d), _addr(slopes),
             code, ws.data_ptr(), ws_bytes)
     return out, lse
 
@@ -657,8 +663,8 @@ def decode_paged_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     slopes = _slopes_for(alibi_slopes, hq, idx)
     _launch(idx, "mea_decode_weights", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             table.data_ptr(), cu.data_ptr(), out.data_ptr(), lse.data_ptr(), weights.data_ptr(),
-            _ptr(prev_weights), width, n, nb, bs, table.size(1), total, max_k, hq, hkv, d,
-            _scale_for(scale, d), _ptr(slopes), code, ws.data_ptr(), ws_bytes, int(split_keys))
+            _addr(prev_weights), width, n, nb, bs, table.size(1), total, max_k, hq, hkv, d,
+            _scale_for(scale, d), _addr(slopes), code, ws.data_ptr(), ws_bytes, int(split_keys))
     return out, lse, weights
 
 
@@ -701,7 +707,7 @@ def attention_packed_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor
     _launch(idx, "mea_attention_weights", q.data_ptr(), k.data_ptr(), lse.data_ptr(),
             cu_q.data_ptr(), cu_k.data_ptr(), weights.data_ptr(), width, n, tq, tk,
             int(max_seqlen_q), max_k, hq, hkv, d, _scale_for(scale, d),
-            _lib.MEA_MASK_CAUSAL if causal else _lib.MEA_MASK_NONE, _ptr(slopes),
+            _lib.MEA_MASK_CAUSAL if causal else _lib.MEA_MASK_NONE, _addr(slopes),
             int(last_queries), _dtype_code(q.dtype), ws.data_ptr(), ws_bytes)
     return weights
 
@@ -799,7 +805,7 @@ def decode_tree_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     _launch(idx, "mea_decode_tree", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             table.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), mask.data_ptr(), out.data_ptr(),
             lse.data_ptr(), n, tq, int(max_seqlen_q), int(max_seqlen_k), mask.size(1), nb, bs,
-            table.size(1), hq, hkv, d, _scale_for(scale, d), _ptr(slopes), code, ws.data_ptr(),
+            table.size(1), hq, hkv, d, _scale_for(scale, d), _addr(slopes), code, ws.data_ptr(),
             ws_bytes)
     return out, lse
 

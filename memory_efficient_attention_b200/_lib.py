@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libmea.so")
@@ -35,9 +36,20 @@ EXPORTS = ("mea_forward", "mea_forward_fp8", "mea_backward_workspace_size", "mea
            "mea_decode_selected_workspace_size", "mea_decode_selected",
            "mea_decode_weights_workspace_size", "mea_decode_weights",
            "mea_attention_weights_workspace_size", "mea_attention_weights",
-           "mea_evict_paged", "mea_decode_tree_workspace_size", "mea_decode_tree",
+           "mea_evict_paged", "mea_decode_tree_workspace_size", "mea_decode_tree", "mea_call",
            "mea_status_string", "mea_device_error",
            "mea_set_wait_timeout_ns", "mea_wait_selftest", "mea_version")
+
+# mea_call: entry number and the words of each call (include/mea.h), the scale as a double.
+CALLS = {
+    "mea_block_key_bounds": (1, struct.Struct("qqqqqqqqqqqqqq")),
+    "mea_select_blocks": (2, struct.Struct("qqqqqqqqqqqqqqqqqq")),
+    "mea_decode_selected": (3, struct.Struct("qqqqqqqqqqqqqqqqdqqqqq")),
+    "mea_decode_weights": (4, struct.Struct("qqqqqqqqqqqqqqqqqqqdqqqqqq")),
+    "mea_attention_weights": (5, struct.Struct("qqqqqqqqqqqqqqqdqqqqqqq")),
+    "mea_evict_paged": (6, struct.Struct("qqqqqqqqqqqqqqqqqqqqqqqqq")),
+    "mea_decode_tree": (7, struct.Struct("qqqqqqqqqqqqqqqqqqqqdqqqqq")),
+}
 
 _lib = None
 
@@ -98,6 +110,8 @@ def load() -> ctypes.CDLL:
     lib.mea_decode_tree_workspace_size.restype = sz
     lib.mea_decode_tree.argtypes = [vp] * 9 + [ci] * 11 + [cf, vp, ci, vp, sz, vp]
     lib.mea_decode_tree.restype = ci
+    lib.mea_call.argtypes = [ci, ctypes.c_char_p]
+    lib.mea_call.restype = ci
     lib.mea_status_string.argtypes = [ci]
     lib.mea_status_string.restype = ctypes.c_char_p
     lib.mea_device_error.argtypes = [ctypes.POINTER(ci), ci]

@@ -214,12 +214,13 @@ int mea_select_blocks(const void* q, const void* bounds, const int32_t* block_ta
   p.n_select = n_select;
   p.n_first = n_first;
   p.n_last = n_last;
+  p.n_seqs = n_seqs;
   p.max_live = static_cast<int>(live);
   // CTAs per (request, head): as many as fill the SMs about twice, and no more than have a round of
-  // 64 blocks to score.
+  // 128 blocks to score.
   const long long pairs = static_cast<long long>(n_seqs) * n_heads_kv;
   int cs = 1;
-  while (cs < 8 && pairs * cs <= di.sms && live > 64ll * cs) cs *= 2;
+  while (cs < 8 && pairs * cs <= di.sms && live > 128ll * cs) cs *= 2;
   constexpr uint32_t max_smem = MEA_SELECT_MAX_BLOCKS * 4u;
   const uint32_t smem = static_cast<uint32_t>(live > 0 ? live : 1) * 4u;
   cudaLaunchConfig_t cfg{};
@@ -234,18 +235,23 @@ int mea_select_blocks(const void* q, const void* bounds, const int32_t* block_ta
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  auto go = [&](auto tag, auto pieces) {
+  auto go = [&](auto tag, auto chunks) {
     constexpr auto kern = mea::mea_select_blocks_kernel<decltype(tag)::value,
-                                                        decltype(pieces)::value>;
+                                                        decltype(chunks)::value>;
     if (smem_attr_once<kern>(max_smem) != cudaSuccess) return MEA_ERR_CUDA;
     clear_stale_launch_error();
     return cudaLaunchKernelEx(&cfg, kern, p) == cudaSuccess ? MEA_OK : MEA_ERR_CUDA;
   };
-  using One = std::integral_constant<int, 1>;
-  using Two = std::integral_constant<int, 2>;
+  using C4 = std::integral_constant<int, 4>;
+  using C8 = std::integral_constant<int, 8>;
+  using C16 = std::integral_constant<int, 16>;
   if (dtype == MEA_BF16)
-    return head_dim > 128 ? go(std::true_type{}, Two{}) : go(std::true_type{}, One{});
-  return head_dim > 128 ? go(std::false_type{}, Two{}) : go(std::false_type{}, One{});
+    return head_dim > 128  ? go(std::true_type{}, C16{})
+           : head_dim > 64 ? go(std::true_type{}, C8{})
+                           : go(std::true_type{}, C4{});
+  return head_dim > 128  ? go(std::false_type{}, C16{})
+         : head_dim > 64 ? go(std::false_type{}, C8{})
+                         : go(std::false_type{}, C4{});
 }
 
 size_t mea_decode_selected_workspace_size(int n_seqs, int n_select, int block_size, int n_heads_q,

@@ -22,6 +22,19 @@ using Half2 = typename std::conditional<BF16, __nv_bfloat162, __half2>::type;
 template <bool BF16>
 using Half1 = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+template <bool BF16>
+__device__ __forceinline__ Half2<BF16> splat_half2(float x) {
+  if constexpr (BF16)
+    return __float2bfloat162_rn(x);
+  else
+    return __float2half2_rn(x);
+}
+
 // ------------------------------------------------------------------------------------------
 // Key ranges: lo[blk, g, d] = min over the block's existing slots of K[slot, g, d], hi = max.
 //
@@ -86,11 +99,9 @@ __global__ void __launch_bounds__(256) mea_key_bounds_kernel(const BoundsParams 
 }
 
 // ------------------------------------------------------------------------------------------
-// The k largest of n 32-bit keys by one CTA of NT threads: radix selection from the top, 11 bits a
-// pass. (Weights and scores share few exponents: 11 bits reach two bits into the mantissa, so that
-// a warp's counts spread over more bins than 8 bits would give them.) Returns the key T of the k-th
-// largest and in `ties` how many of the keys equal to T belong to the k (the caller takes the lowest
-// indices of them). 1 <= k <= n.
+// The k largest of n 32-bit keys by one CTA: radix selection of key - min, 8 bits a pass from the
+// highest bit in which the keys differ at all. (Weights and scores share their leading bits: taken
+// as they are, a pass counted all keys in a few bins, one after the other.)
 // ------------------------------------------------------------------------------------------
 // Order-preserving image of an fp32 value (as unsigned; -0 equals +0). NaN ranks above all.
 __device__ __forceinline__ uint32_t rank_key(float x) {
@@ -105,7 +116,8 @@ __device__ __forceinline__ float rank_value(uint32_t k) {
 constexpr uint32_t kRankAlways = 0xFFFFFFFFu;  // ranks above every value
 
 struct SelectScratch {
-  int hist[2048];
+  int hist[2048];  // 4 x 256, one histogram a pass, or 2048 bins
+  uint32_t least[32], most[32];
   int sum[2][32];
   int bin, above;
 };
@@ -124,8 +136,90 @@ __device__ __forceinline__ int warps_before(const int* sum) {
   return __shfl_sync(0xffffffffu, incl - v, warp);
 }
 
+// Returns the key T of the k-th largest (or one below it) and in `ties` how many of the keys equal to
+// T belong to the k (the caller takes the lowest indices of them, beside all keys above T).
+// 1 <= k <= n. Every pass costs one barrier: it has its own histogram, and every warp scans it.
 template <int NT, class Get>
 __device__ __forceinline__ uint32_t radix_select(Get get, int n, int k, SelectScratch& sc,
+                                                 int& ties) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < 4 * 256; i += NT) sc.hist[i] = 0;
+  uint32_t lo = 0xFFFFFFFFu, hi = 0u;
+#pragma unroll 4
+  for (int i = tid; i < n; i += NT) {
+    const uint32_t x = get(i);
+    if (x != kRankAlways) {  // (far above all others: they would take the first digits' range)
+      lo = min(lo, x);
+      hi = max(hi, x);
+    }
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    sc.least[warp] = lo;
+    sc.most[warp] = hi;
+  }
+  __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, lane < NT / 32 ? sc.least[lane] : 0xFFFFFFFFu);
+  hi = __reduce_max_sync(0xffffffffu, lane < NT / 32 ? sc.most[lane] : 0u);
+  ties = k;
+  if (lo > hi) return kRankAlways;  // no other keys
+  const uint32_t top = hi + 1u;     // stands for kRankAlways below
+  uint32_t prefix = 0, high = 0;
+  int need = k;
+  int shift = max(24 - __clz(static_cast<int>(top - lo)), 0);
+  for (int pass = 0;; ++pass) {
+    int* h = sc.hist + 256 * pass;
+#pragma unroll 4
+    for (int i = tid; i < n; i += NT) {
+      const uint32_t x = min(get(i), top) - lo;
+      if ((x & high) == prefix) atomicAdd(&h[(x >> shift) & 255u], 1);
+    }
+    __syncthreads();
+    int c[8], sum = 0;  // bins 255 - 8 lane, ... downwards
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      c[i] = h[255 - (lane * 8 + i)];
+      sum += c[i];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += y;
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, incl >= need)) - 1;
+    int above = incl - sum, bin = 0, in = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (in == 0 && above + c[i] >= need) {
+        bin = 255 - (lane * 8 + i);
+        in = c[i];
+      }
+      if (in == 0) above += c[i];
+    }
+    bin = __shfl_sync(0xffffffffu, bin, src);
+    in = __shfl_sync(0xffffffffu, in, src);
+    need -= __shfl_sync(0xffffffffu, above, src);
+    prefix |= static_cast<uint32_t>(bin) << shift;
+    if (need == in) {  // the whole bin belongs: everything from its least value on
+      ties = 0;
+      return prefix + lo - 1u;  // (rank keys are above 0)
+    }
+    if (shift == 0) break;
+    const int next = max(shift - 8, 0);
+    high = 0xFFFFFFFFu << shift;
+    shift = next;
+  }
+  ties = need;
+  return prefix + lo == top ? kRankAlways : prefix + lo;
+}
+
+// The same for many keys that spread over a few binades, as attention weights do: 11 bits a pass from
+// the top, the bins shared out over the threads. 16384 weights in 1024 threads: 10 % less time than
+// the above, which reads them once more and has more passes.
+template <int NT, class Get>
+__device__ __forceinline__ uint32_t radix_select_wide(Get get, int n, int k, SelectScratch& sc,
                                                  int& ties) {
   constexpr int PER = 2048 / NT;  // bins per thread
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -225,10 +319,14 @@ __device__ __forceinline__ void compact_selected(Get get, Put put, int n, uint32
 // the bound of a sum of heads is linear in (up, down). The scores are summed in 64 bits and rounded
 // to 32 once: then the order of summation does not show in the choice.
 //
-// Bound by reading the ranges (4 D bytes a block and head). A cluster of CTAs serves one (request,
-// KV head): each CTA's warps score a share of its blocks (a warp reads a block's two rows with
-// one 16-byte load a lane, eight blocks in flight, and adds the eight sums up together) and leave
-// the rank keys in the first CTA's shared memory, which then selects.
+// Bound by reading the ranges (4 D bytes a block and head); in 64 bits throughout, the conversions and
+// products took three times as long as that. So the scores are first computed on the tensor cores
+// (mma.sync, 16 blocks a tile, w = (down, up) as three 16-bit pieces in three of the eight columns,
+// fp32 sums), which is off by at most delta = 2^-16 sum|w| max|range| (48 products' sums of 2^-23 at
+// most each, with room), and the blocks within 2 delta of the cut, one or two as a rule, are scored
+// again in 64 bits: a block further above (below) the cut than that is above (below) it in 64 bits too.
+// A cluster of CTAs serves one (request, KV head): each CTA's warps score a share of its blocks and
+// leave the rank keys in the first CTA's shared memory, which then selects.
 // ------------------------------------------------------------------------------------------
 struct SelectParams {
   const void* q;       // [n_seqs, hq, D]
@@ -237,6 +335,7 @@ struct SelectParams {
   const int32_t* cu_k;
   int32_t* selected;   // [n_seqs, hkv, n_select]
   int num_blocks, block_size, max_blocks, hq, hkv, dh, n_select, n_first, n_last;
+  int n_seqs;
   int max_live;        // bound on a request's blocks: rank keys in shared memory
 };
 
@@ -247,21 +346,51 @@ __device__ __forceinline__ float half_f32(uint32_t w, int i) {
   const Half2<BF16> h = *reinterpret_cast<const Half2<BF16>*>(&w);
   return i ? __high2float(h) : __low2float(h);
 }
+template <bool BF16>
+__device__ __forceinline__ uint32_t half_bits(float x) {
+  const Half1<BF16> h = static_cast<Half1<BF16>>(x);
+  return *reinterpret_cast<const unsigned short*>(&h);
+}
 
-// PIECES: 16-byte pieces of a block's two rows per lane (1 up to head dim 128, 2 above).
-template <bool BF16, int PIECES>
-__global__ void __launch_bounds__(kSelThreads, PIECES == 1 ? 3 : 2)
+// CHUNKS: 32-element pieces of a block's two rows (2 D elements), 4, 8 or 16.
+template <bool BF16, int CHUNKS>
+__global__ void __launch_bounds__(kSelThreads, CHUNKS == 16 ? 1 : 2)
     mea_select_blocks_kernel(const SelectParams p) {
   namespace cg = cooperative_groups;
   auto cluster = cg::this_cluster();
   const int cs = static_cast<int>(cluster.num_blocks());
   const int cr = static_cast<int>(cluster.block_rank());
   const int pair = blockIdx.x / cs;
-  const int b = pair / p.hkv, g = pair - b * p.hkv;
   const int R = p.hq / p.hkv;
   extern __shared__ __align__(16) uint32_t s_keys[];
   __shared__ double s_w[2 * 256];  // [down][up]
+  // w's 16-bit pieces as B fragments: [chunk][lane][4 words] (lanes 4 n + t4, n < 3, hold piece n)
+  __shared__ __align__(16) uint32_t s_frag[CHUNKS * 32 * 4];
+  __shared__ int s_again[32];
+  __shared__ float s_most[8 * (kSelThreads / 32)];  // max |range| by warp of the cluster
   __shared__ SelectScratch s_sc;
+  const int g = pair % p.hkv;
+  int b = pair / p.hkv;
+  pdl_trigger();
+  // The longest requests first, so that no long one starts last (each CTA ranks the lengths; lists
+  // too long for that go in their order).
+  if (p.n_seqs > 1 && p.n_seqs <= kSelThreads) {
+    int* len = reinterpret_cast<int*>(s_w);
+    int mine = 0;
+    if (threadIdx.x < p.n_seqs) {
+      mine = __ldg(p.cu_k + threadIdx.x + 1) - __ldg(p.cu_k + threadIdx.x);
+      len[threadIdx.x] = mine;
+    }
+    __syncthreads();
+    if (threadIdx.x < p.n_seqs) {
+      int rank = 0;
+      for (int t = 0; t < p.n_seqs; ++t)
+        rank += len[t] > mine || (len[t] == mine && t < static_cast<int>(threadIdx.x));
+      if (rank == b) s_sc.sum[0][0] = threadIdx.x;
+    }
+    __syncthreads();
+    b = s_sc.sum[0][0];
+  }
   const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
   const int nblk = min((L + p.block_size - 1) / p.block_size, min(p.max_blocks, p.max_live));
   int32_t* out = p.selected + (static_cast<size_t>(b) * p.hkv + g) * p.n_select;
@@ -277,25 +406,31 @@ __global__ void __launch_bounds__(kSelThreads, PIECES == 1 ? 3 : 2)
   const int np = p.dh / 4;  // 16-byte pieces of a block's ranges
   const int32_t* row = p.block_table + static_cast<size_t>(b) * p.max_blocks;
   const uint4* bounds = static_cast<const uint4*>(p.bounds);
-  constexpr int U = 8;  // blocks in flight per warp
-  const int stride = cs * (kSelThreads / 32) * U;
-  int j0 = (cr * (kSelThreads / 32) + warp) * U;
-  auto block_id = [&](int j) { return (lane < U && j + lane < nblk) ? __ldg(row + j + lane) : -1; };
-  uint4 v[U][PIECES];
-  auto load = [&](int ids) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int id = __shfl_sync(0xffffffffu, ids, u);
-      const bool in = id >= 0 && id < p.num_blocks;
-      const uint4* src = bounds + (static_cast<size_t>(in ? id : 0) * p.hkv + g) * np;
-#pragma unroll
-      for (int c = 0; c < PIECES; ++c)
-        v[u][c] = (in && lane + 32 * c < np) ? __ldg(src + lane + 32 * c)
-                                             : make_uint4(0u, 0u, 0u, 0u);
-    }
+  const int g8 = lane >> 2, t4 = lane & 3;
+  const int stride = cs * (kSelThreads / 32) * 16;
+  const int jw = (cr * (kSelThreads / 32) + warp) * 16;
+  // Rows g8 and g8 + 8 of a tile are blocks j + g8, j + g8 + 8; lane t4 reads pieces t4, t4 + 4, ... of
+  // them (the sum does not mind which lane has which columns, as long as w goes by the same order).
+  auto block_id = [&](int j) { return j < nblk ? __ldg(row + j) : -1; };
+  auto source = [&](int id) {
+    return (id >= 0 && id < p.num_blocks)
+               ? bounds + (static_cast<size_t>(id) * p.hkv + g) * np + t4
+               : nullptr;
   };
-  load(block_id(j0));
-  int ids = block_id(j0 + stride);
+  uint4 v[CHUNKS][2];  // a whole tile; a chunk's registers take the next tile's as soon as it is used
+  const uint4 *s0 = nullptr, *s1 = nullptr;
+  auto load = [&](int c) {
+    const bool in = c * 4 + t4 < np;
+    v[c][0] = in && s0 ? __ldg(s0 + c * 4) : make_uint4(0u, 0u, 0u, 0u);
+    v[c][1] = in && s1 ? __ldg(s1 + c * 4) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  s0 = source(block_id(jw + g8));
+  s1 = source(block_id(jw + g8 + 8));
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) load(c);
+  int id0 = block_id(jw + stride + g8), id1 = block_id(jw + stride + g8 + 8);
+  for (int i = tid; i < CHUNKS * 128; i += kSelThreads) s_frag[i] = 0u;
+  __syncthreads();
   // up and down, while the first blocks are on their way
   const Half1<BF16>* q =
       static_cast<const Half1<BF16>*>(p.q) + (static_cast<size_t>(b) * p.hq + g * R) * p.dh;
@@ -309,63 +444,178 @@ __global__ void __launch_bounds__(kSelThreads, PIECES == 1 ? 3 : 2)
     }
     s_w[d] = down;
     s_w[p.dh + d] = up;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      double x = e ? up : down;
+#pragma unroll
+      for (int n = 0; n < 3; ++n) {
+        const uint32_t bits = half_bits<BF16>(static_cast<float>(x));
+        const int k = e * p.dh + d;  // column of (down, up): chunk k / 32, lane's piece (k / 8) % 4
+        reinterpret_cast<unsigned short*>(
+            s_frag)[(((k >> 5) * 32 + n * 4 + ((k >> 3) & 3)) * 4 + ((k >> 1) & 3)) * 2 + (k & 1)] =
+            static_cast<unsigned short>(bits);
+        x -= static_cast<double>(half_f32<BF16>(bits, 0));
+      }
+    }
   }
   __syncthreads();
-  double w[PIECES][8];
-#pragma unroll
-  for (int c = 0; c < PIECES; ++c)
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      w[c][i] = lane + 32 * c < np ? s_w[(lane + 32 * c) * 8 + i] : 0.0;
   if (cs > 1) cluster.barrier_wait();
   uint32_t* keys = cs > 1 ? cluster.map_shared_rank(s_keys, 0) : s_keys;
-  for (; j0 < nblk; j0 += stride) {
-    double s[U];
+  Half2<BF16> most = splat_half2<BF16>(0.f);
+  for (int j = jw; j < nblk; j += stride) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f};
+    s0 = source(id0);
+    s1 = source(id1);
+    id0 = block_id(j + 2 * stride + g8);
+    id1 = block_id(j + 2 * stride + g8 + 8);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      s[u] = 0.0;
+    for (int c = 0; c < CHUNKS; ++c) {
+      const uint32_t x[2][4] = {{v[c][0].x, v[c][0].y, v[c][0].z, v[c][0].w},
+                                {v[c][1].x, v[c][1].y, v[c][1].z, v[c][1].w}};
+      const uint32_t a0[4] = {x[0][0], x[1][0], x[0][1], x[1][1]};
+      const uint32_t a1[4] = {x[0][2], x[1][2], x[0][3], x[1][3]};
+      const uint4 w = *reinterpret_cast<const uint4*>(&s_frag[(c * 32 + lane) * 4]);
+      mma16816<BF16>(acc, a0, w.x, w.y);
+      mma16816<BF16>(acc, a1, w.z, w.w);
 #pragma unroll
-      for (int c = 0; c < PIECES; ++c) {
-        const uint32_t x[4] = {v[u][c].x, v[u][c].y, v[u][c].z, v[u][c].w};
+      for (int i = 0; i < 4; ++i) {
+        most = __hmax2_nan(most, __habs2(*reinterpret_cast<const Half2<BF16>*>(&x[0][i])));
+        most = __hmax2_nan(most, __habs2(*reinterpret_cast<const Half2<BF16>*>(&x[1][i])));
+      }
+      load(c);
+    }
+    // Columns 0 and 1 are lane t4 = 0's, column 2 lane t4 = 1's.
+    const float third0 = __shfl_down_sync(0xffffffffu, acc[0], 1);
+    const float third1 = __shfl_down_sync(0xffffffffu, acc[2], 1);
+    if (t4 == 0) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          s[u] = fma(w[c][i], static_cast<double>(half_f32<BF16>(x[i >> 1], i & 1)), s[u]);
+      for (int h = 0; h < 2; ++h) {
+        const int i = j + g8 + 8 * h;
+        const float x = h ? (acc[2] + acc[3]) + third1 : (acc[0] + acc[1]) + third0;
+        const bool always = i < p.n_first || i >= nblk - p.n_last;
+        if (i < nblk) keys[i] = always ? kRankAlways : rank_key(x);
       }
     }
-    load(ids);
-    ids = block_id(j0 + 2 * stride);
-    // Eight sums over the warp at once: each step halves how many a lane carries.
+  }
+  {
+    float m = max_nan(__low2float(most), __high2float(most));
 #pragma unroll
-    for (int half = U / 2, off = 16; half >= 1; half >>= 1, off >>= 1) {
-      const bool hi = (lane & off) != 0;
-#pragma unroll
-      for (int u = 0; u < U / 2; ++u) {
-        if (u < half) {
-          const double give = hi ? s[u] : s[u + half];
-          const double keep = hi ? s[u + half] : s[u];
-          s[u] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-        }
-      }
-    }
-    // (bit 4 of the lane chose the upper four blocks, bit 3 the upper two of four, bit 2 the odd one)
-    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 2);
-    s[0] += __shfl_xor_sync(0xffffffffu, s[0], 1);
-    const int j = j0 + (lane >> 2);
-    if ((lane & 3) == 0 && j < nblk) {
-      const bool always = j < p.n_first || j >= nblk - p.n_last;
-      keys[j] = always ? kRankAlways : rank_key(static_cast<float>(s[0]));
-    }
+    for (int off = 16; off > 0; off >>= 1)
+      m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, off));
+    float* dst = cs > 1 ? cluster.map_shared_rank(s_most, 0) : s_most;
+    if (lane == 0) dst[cr * (kSelThreads / 32) + warp] = m;
   }
   if (cs > 1)
     cluster.sync();
   else
     __syncthreads();
   if (cr != 0) return;
-  int ties = 0;
   auto get = [&](int i) { return s_keys[i]; };
-  const uint32_t T = radix_select<kSelThreads>(get, nblk, p.n_select, s_sc, ties);
-  compact_selected<kSelThreads>(get, [&](int at, int i, uint32_t) { out[at] = i; }, nblk, T, ties,
-                                s_sc);
+  auto put = [&](int at, int i, uint32_t) { out[at] = i; };
+  int ties = 0;
+  uint32_t T = radix_select<kSelThreads>(get, nblk, p.n_select, s_sc, ties);
+  if (T != kRankAlways) {
+    // delta, in every warp
+    float most_all = 0.f, sum_w = 0.f;
+    for (int i = lane; i < cs * (kSelThreads / 32); i += 32) most_all = max_nan(most_all, s_most[i]);
+    for (int d = lane; d < 2 * p.dh; d += 32) sum_w += fabsf(static_cast<float>(s_w[d]));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+      most_all = max_nan(most_all, __shfl_xor_sync(0xffffffffu, most_all, off));
+      sum_w += __shfl_xor_sync(0xffffffffu, sum_w, off);
+    }
+    // (the last term: third pieces below a half's smallest step; a NaN or an infinity in the ranges
+    // or the queries makes delta one, and every block is scored again)
+    const float delta = 0x1p-16f * sum_w * most_all + 0x1p-15f * most_all;
+    const float cut = rank_value(T);
+    const float above = cut + 2.f * delta, below = cut - 2.f * delta;
+    const bool sane = delta < 0x1p120f;
+    // Keys become "in", 1 (out) or 2 (to be scored again).
+    int n_in = 0, n_again = 0;
+    for (int i = tid; i < nblk; i += kSelThreads) {
+      const uint32_t x = s_keys[i];
+      uint32_t to = kRankAlways;
+      if (x != kRankAlways) {
+        const float f = rank_value(x);
+        if (!(sane && f > above)) to = sane && f < below ? 1u : 2u;
+      }
+      s_keys[i] = to;
+      n_in += to == kRankAlways;
+      n_again += to == 2u;
+    }
+    n_in = __reduce_add_sync(0xffffffffu, n_in);
+    n_again = __reduce_add_sync(0xffffffffu, n_again);
+    __syncthreads();  // (the selection's sums have been read)
+    if (lane == 0) {
+      s_sc.sum[0][warp] = n_in;
+      s_sc.sum[1][warp] = n_again;
+    }
+    __syncthreads();
+    n_in = __reduce_add_sync(0xffffffffu, lane < kSelThreads / 32 ? s_sc.sum[0][lane] : 0);
+    n_again = __reduce_add_sync(0xffffffffu, lane < kSelThreads / 32 ? s_sc.sum[1][lane] : 0);
+    T = 1u;  // keys above: "in", and those marked 2 where all of them belong
+    ties = 0;
+    if (n_in + n_again != p.n_select) {
+      auto exact = [&](int i) {  // warp-cooperative
+        const int id = __ldg(row + i);
+        const uint4* src = (id >= 0 && id < p.num_blocks)
+                               ? bounds + (static_cast<size_t>(id) * p.hkv + g) * np
+                               : nullptr;
+        double x = 0.0;
+        for (int c = lane; src && c < np; c += 32) {
+          const uint4 r = __ldg(src + c);
+          const uint32_t w4[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            x = fma(s_w[c * 8 + e], static_cast<double>(half_f32<BF16>(w4[e >> 1], e & 1)), x);
+        }
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
+        return rank_key(static_cast<float>(x));
+      };
+      if (n_again <= 32) {
+        // A list of them in order, a warp each, and one warp that ranks them.
+        if (warp == 0) {
+          int n = 0;
+          for (int i0 = 0; i0 < nblk; i0 += 32) {
+            const bool mine = i0 + lane < nblk && s_keys[i0 + lane] == 2u;
+            const unsigned m = __ballot_sync(0xffffffffu, mine);
+            if (mine) s_again[n + __popc(m & ((1u << lane) - 1u))] = i0 + lane;
+            n += __popc(m);
+          }
+        }
+        __syncthreads();
+        for (int a = warp; a < n_again; a += kSelThreads / 32) {
+          const uint32_t x = exact(s_again[a]);
+          if (lane == 0) s_sc.hist[a] = static_cast<int>(x);
+        }
+        __syncthreads();
+        if (warp == 0 && lane < n_again) {
+          const uint32_t x = static_cast<uint32_t>(s_sc.hist[lane]);
+          int rank = 0;
+          for (int a = 0; a < n_again; ++a) {
+            const uint32_t y = static_cast<uint32_t>(s_sc.hist[a]);
+            rank += y > x || (y == x && a < lane);
+          }
+          s_keys[s_again[lane]] = n_in + rank < p.n_select ? kRankAlways : 1u;
+        }
+      } else {
+        for (int i0 = warp * 32; i0 < nblk; i0 += kSelThreads) {
+          unsigned again = __ballot_sync(0xffffffffu, i0 + lane < nblk && s_keys[i0 + lane] == 2u);
+          while (again) {
+            const int i = i0 + __ffs(again) - 1;
+            again &= again - 1;
+            const uint32_t x = exact(i);
+            if (lane == 0) s_keys[i] = x;
+          }
+        }
+        __syncthreads();
+        T = radix_select<kSelThreads>(get, nblk, p.n_select, s_sc, ties);
+      }
+    }
+  }
+  __syncthreads();
+  compact_selected<kSelThreads>(get, put, nblk, T, ties, s_sc);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -452,11 +702,11 @@ __global__ void __launch_bounds__(kEvictThreads) mea_evict_select_kernel(const E
       }
       __syncthreads();
       auto get = [&](int i) { return s_keys[i]; };
-      const uint32_t T = radix_select<kEvictThreads>(get, m, k, s_sc, ties);
+      const uint32_t T = radix_select_wide<kEvictThreads>(get, m, k, s_sc, ties);
       compact_selected<kEvictThreads>(get, put, m, T, ties, s_sc);
     } else {
       auto get = [&](int i) { return rank_key(__ldg(w + i)); };
-      const uint32_t T = radix_select<kEvictThreads>(get, m, k, s_sc, ties);
+      const uint32_t T = radix_select_wide<kEvictThreads>(get, m, k, s_sc, ties);
       compact_selected<kEvictThreads>(get, put, m, T, ties, s_sc);
     }
   }

@@ -159,14 +159,14 @@ struct DecRange {
   __device__ __forceinline__ void init(const DecParams& p, int grid, int cta) {
     T = p.item_tiles;
     const long long total = p.n_items * T;
-    const long long per = (total + grid - 1) / grid;
+    const long long per = div_nn(total + grid - 1, grid);
     start = pos = per * cta;
     end = min(total, pos + per);
   }
   // The next item, its tiles [t0, t1) and where its partial goes (-1: the whole item).
   __device__ __forceinline__ bool next(long long& item, int& t0, int& t1, int& slot, int cta) {
     if (pos >= end) return false;
-    item = pos / T;
+    item = div_nn(pos, T);
     t0 = static_cast<int>(pos - item * T);
     t1 = static_cast<int>(min(static_cast<long long>(T), t0 + (end - pos)));
     slot = (t0 == 0 && t1 == T) ? -1 : 2 * cta + (pos == start ? 0 : 1);
@@ -250,7 +250,8 @@ __global__ void __launch_bounds__(160, 1)
       if constexpr (MODE == DEC_SELECTED) {
         if (!range.next(item, t0, t1, slot, blockIdx.x)) break;
       }
-      const int cid = static_cast<int>(item / p.n_hb);
+      const int cid = static_cast<int>(MODE == DEC_SELECTED ? div_nn(item, p.n_hb)
+                                                            : item / p.n_hb);
       const int hb = static_cast<int>(item - static_cast<long long>(cid) * p.n_hb);
       int b = cid, c = 0;
       if constexpr (MODE != DEC_SELECTED) {
@@ -375,7 +376,8 @@ __global__ void __launch_bounds__(160, 1)
       if constexpr (MODE == DEC_SELECTED) {
         if (!range.next(item, t0, t1, part, blockIdx.x)) break;
       }
-      const int cid = static_cast<int>(item / p.n_hb);
+      const int cid = static_cast<int>(MODE == DEC_SELECTED ? div_nn(item, p.n_hb)
+                                                            : item / p.n_hb);
       const int hb = static_cast<int>(item - static_cast<long long>(cid) * p.n_hb);
       int b = cid, c = 0;
       if constexpr (MODE != DEC_SELECTED) {
@@ -755,15 +757,15 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(256) mea_selected_merge_kernel(const DecParams p, int grid) {
   pdl_wait();
   const long long T = p.item_tiles, total = p.n_items * T;
-  const long long per = (total + grid - 1) / grid;
+  const long long per = div_nn(total + grid - 1, grid);
   const long long pos = per * (blockIdx.x + 1);
   if (pos >= total) return;
-  const long long item = pos / T, i0 = item * T;
+  const long long item = div_nn(pos, T), i0 = item * T;
   if (i0 == pos || i0 < pos - per) return;  // not crossed here, or first crossed earlier
-  const int c0 = blockIdx.x, c1 = static_cast<int>((i0 + T - 1) / per);
+  const int c0 = blockIdx.x, c1 = static_cast<int>(div_nn(i0 + T - 1, per));
   // CTA c0's part is its first range only when the item starts there; later CTAs' always is.
   const int skip = i0 == pos - per ? 0 : 1;
-  const int b = static_cast<int>(item / p.n_hb);
+  const int b = static_cast<int>(div_nn(item, p.n_hb));
   const int hb = static_cast<int>(item - static_cast<long long>(b) * p.n_hb);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   using OutT = typename std::conditional<BF16, __nv_bfloat16, __half>::type;

@@ -429,6 +429,14 @@ __host__ __device__ constexpr uint32_t umma_idesc_e4m3(int M, int N, bool a_mn, 
          (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
+// Quotient of non-negative 64-bit values, by the 32-bit division (a quarter of the 64-bit one's
+// latency) when both fit it.
+__device__ __forceinline__ long long div_nn(long long a, long long b) {
+  if (((a | b) >> 32) == 0)
+    return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 // ------------------------------------------------------------------------------------------
 // Math helpers. f32x2 operations work on a pair of fp32 values held in one 64-bit register.
 // ------------------------------------------------------------------------------------------

@@ -152,7 +152,7 @@ struct TreeWalk {
   TreeSeq s;
   __device__ __forceinline__ void init(const TreeParams& p) {
     const long long total = tree_total<ROWS>(p);
-    const long long per = (total + gridDim.x - 1) / gridDim.x;
+    const long long per = div_nn(total + gridDim.x - 1, gridDim.x);
     start = pos = per * blockIdx.x;
     end = min(total, pos + per);
     b = p.n_seqs;
@@ -168,7 +168,7 @@ struct TreeWalk {
       s = tree_seq<ROWS>(p, ++b);
     }
     const long long off = pos - base;
-    const int item = static_cast<int>(off / s.tiles);
+    const int item = static_cast<int>(div_nn(off, s.tiles));
     f.t0 = static_cast<int>(off - static_cast<long long>(item) * s.tiles);
     f.t1 = static_cast<int>(min(static_cast<long long>(s.tiles), f.t0 + (end - pos)));
     f.g = item / s.parts;
@@ -810,18 +810,18 @@ __global__ void __launch_bounds__(256) mea_tree_merge_kernel(const TreeParams p,
   constexpr int ROWS = C::ROWS;
   pdl_wait();
   const long long total = tree_total<ROWS>(p);
-  const long long per = (total + grid - 1) / grid;
+  const long long per = div_nn(total + grid - 1, grid);
   const long long pos = per * (blockIdx.x + 1);
   if (pos >= total) return;
   long long base = 0;
   const int b = tree_find<ROWS>(p, pos, base);
   const TreeSeq s = tree_seq<ROWS>(p, b);
-  const int item = static_cast<int>((pos - base) / s.tiles);
+  const int item = static_cast<int>(div_nn(pos - base, s.tiles));
   const long long i0 = base + static_cast<long long>(item) * s.tiles;  // the item's tiles
   const long long i1 = i0 + s.tiles;
   if (i0 == pos || i0 < pos - per) return;  // not crossed here, or first crossed earlier
   const int c0 = blockIdx.x;
-  const int c1 = static_cast<int>((i1 - 1) / per);  // last CTA with a part
+  const int c1 = static_cast<int>(div_nn(i1 - 1, per));  // last CTA with a part
   const int g = item / s.parts;
   const int row0 = (item - g * s.parts) * ROWS;
   const int rows = min(ROWS, s.nq * p.R - row0);

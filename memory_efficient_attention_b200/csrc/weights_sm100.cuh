@@ -191,7 +191,7 @@ struct WeightsWalk {
   }
   __device__ __forceinline__ void init(const WeightsParams& p, int grid, int cta) {
     const long long total = weights_total<KT, CAUSAL>(p);
-    const long long per = (total + grid - 1) / grid;
+    const long long per = div_nn(total + grid - 1, grid);
     start = pos = per * cta;
     end = min(total, pos + per);
     if (pos >= end) return;
@@ -201,7 +201,7 @@ struct WeightsWalk {
     pos = at;
     seg = weights_find<KT, CAUSAL>(p, at, base);
     s = weights_seq<KT, CAUSAL>(p, seg);
-    g = static_cast<int>((at - base) / s.work);
+    g = static_cast<int>(div_nn(at - base, s.work));
     base += s.work * g;
     // The last item that starts at or before `at`.
     const int hbn = p.R >> p.log2_p;
@@ -615,14 +615,14 @@ __global__ void __launch_bounds__(WeightsCfg<D>::KT)
   constexpr int KT = WeightsCfg<D>::KT;
   pdl_wait();
   const long long total = weights_total<KT, CAUSAL>(p);
-  const long long per = (total + grid - 1) / grid;
+  const long long per = div_nn(total + grid - 1, grid);
   const long long pos = per * (blockIdx.x + 1);
   if (pos >= total) return;
   WeightsWalk<KT, CAUSAL> w;
   w.seek(p, pos);
   if (w.base == pos || w.base < pos - per) return;  // not crossed here, or first crossed earlier
   const int c0 = blockIdx.x;
-  const int c1 = static_cast<int>((w.base + w.len - 1) / per);  // last CTA with a part
+  const int c1 = static_cast<int>(div_nn(w.base + w.len - 1, per));  // last CTA with a part
   // CTA c0's part is its first range only when the item starts there; later CTAs' always is.
   const int skip = w.base == pos - per ? 0 : 1;
   const int row = threadIdx.x;
