@@ -275,6 +275,27 @@ __device__ __forceinline__ uint32_t radix_select_wide(Get get, int n, int k, Sel
   return prefix;
 }
 
+// The request of rank `r` by length, longest first (equal ones by index), so that CTAs in rank order
+// leave no long request to the end. n <= the CTA's threads; len[n] and found[1] in shared memory.
+__device__ __forceinline__ int nth_longest(const int32_t* cu, int n, int r, int* len, int* found) {
+  const int t = threadIdx.x;
+  int mine = 0;
+  if (t < n) {
+    mine = __ldg(cu + t + 1) - __ldg(cu + t);
+    len[t] = mine;
+  }
+  __syncthreads();
+  if (t < n) {
+    int rank = 0;
+    for (int u = 0; u < n; ++u) rank += len[u] > mine || (len[u] == mine && u < t);
+    if (rank == r) found[0] = t;
+  }
+  __syncthreads();
+  const int b = found[0];
+  __syncthreads();
+  return b;
+}
+
 // Hands the indices of the keys above T, and of the first `ties` keys equal to T, in ascending
 // order to put(place, index, key). A warp takes a contiguous part: it counts, the counts are added up
 // over the warps, then it places.
@@ -372,25 +393,8 @@ __global__ void __launch_bounds__(kSelThreads, CHUNKS == 16 ? 1 : 2)
   const int g = pair % p.hkv;
   int b = pair / p.hkv;
   pdl_trigger();
-  // The longest requests first, so that no long one starts last (each CTA ranks the lengths; lists
-  // too long for that go in their order).
-  if (p.n_seqs > 1 && p.n_seqs <= kSelThreads) {
-    int* len = reinterpret_cast<int*>(s_w);
-    int mine = 0;
-    if (threadIdx.x < p.n_seqs) {
-      mine = __ldg(p.cu_k + threadIdx.x + 1) - __ldg(p.cu_k + threadIdx.x);
-      len[threadIdx.x] = mine;
-    }
-    __syncthreads();
-    if (threadIdx.x < p.n_seqs) {
-      int rank = 0;
-      for (int t = 0; t < p.n_seqs; ++t)
-        rank += len[t] > mine || (len[t] == mine && t < static_cast<int>(threadIdx.x));
-      if (rank == b) s_sc.sum[0][0] = threadIdx.x;
-    }
-    __syncthreads();
-    b = s_sc.sum[0][0];
-  }
+  if (p.n_seqs > 1 && p.n_seqs <= kSelThreads)
+    b = nth_longest(p.cu_k, p.n_seqs, b, reinterpret_cast<int*>(s_w), s_sc.sum[0]);
   const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
   const int nblk = min((L + p.block_size - 1) / p.block_size, min(p.max_blocks, p.max_live));
   int32_t* out = p.selected + (static_cast<size_t>(b) * p.hkv + g) * p.n_select;

@@ -21,7 +21,9 @@
 // result is deterministic.
 //
 // Roles: warp 16 the tcgen05 issuer, warp 17 the TMA producer, warp 18 the columns' terms (log-sum-exp
-// and ALiBi), warpgroups 0-3 the sums: warpgroup w takes key tile w % SUBS of every NBUF-th step (a
+// and ALiBi), warp 19 the schedule (it hands the CTA's ranges, decoded, to the others through a small
+// queue in shared memory: walked by every warp, the line cost a short range's warps more than its
+// exponentials), warpgroups 0-3 the sums: warpgroup w takes key tile w % SUBS of every NBUF-th step (a
 // step costs a warp about 100 instructions beside its columns', so half tiles of every step are
 // slower).
 //
@@ -67,7 +69,9 @@ struct WeightsCfg {
   static constexpr uint32_t SMEM_T = SMEM_Q + NQ * TILE_BYTES;   // 2 NBUF x 3 x 128 floats
   static constexpr uint32_t SMEM_SUM = SMEM_T + 2 * NBUF * 3 * 512;  // 3 warpgroups x 128 floats
   static constexpr uint32_t SMEM_MISC = SMEM_SUM + 3 * 512;
-  static constexpr uint32_t SMEM_TOTAL = SMEM_MISC + 256 + 1024;
+  static constexpr int QD = 4;                   // ranges in the queue, 64 bytes each
+  static constexpr uint32_t MISC_QUEUE = 256;
+  static constexpr uint32_t SMEM_TOTAL = SMEM_MISC + MISC_QUEUE + QD * 64 + 1024;
   static_assert(SMEM_TOTAL <= 232448, "shared memory per CTA");
   static constexpr int THREADS = 640;
   // Launched at 96 registers a thread (640 x 96 = 61440): the warps beside the sums give theirs down
@@ -84,6 +88,12 @@ struct WeightsFrag {
   int s0, s1;                      // steps [s0, s1); step s is head block s / nt, Q tile s % nt
   bool whole, first;
 };
+
+// A range in the queue, as 32-bit words (flags 0 ends the list).
+struct WeightsEntry {
+  int seg, g, q0, lq, k0, lk, j0, qbeg, nt, s0, s1, flags;
+};
+enum : int { WF_LIVE = 1, WF_WHOLE = 2, WF_FIRST = 4 };
 
 // A segment's items: items before n0 have queries [qw, lq) and nt0 Q tiles; under a causal mask those
 // from n0 on start at their first key's own query, and have a - kt * (KT / QT) Q tiles (KT is a
@@ -295,7 +305,6 @@ __global__ void __launch_bounds__(640, 1)
     mea_weights_sm100_kernel(const __grid_constant__ CUtensorMap tm_q,
                              const __grid_constant__ CUtensorMap tm_k, const WeightsParams p) {
   using C = WeightsCfg<D>;
-  using Walk = WeightsWalk<C::KT, CAUSAL>;
   constexpr float LOG2E = 1.4426950408889634f;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   const uint32_t pad = (1024u - (smem_u32(smem_raw) & 1023u)) & 1023u;
@@ -303,9 +312,9 @@ __global__ void __launch_bounds__(640, 1)
   const uint32_t sbase = smem_u32(smem);
   constexpr int B_KF = 0, B_KE = B_KF + C::NK, B_QF = B_KE + C::NK, B_QE = B_QF + C::NQ;
   constexpr int B_SF = B_QE + C::NQ, B_SE = B_SF + 4, B_CF = B_SE + 4;  // S: per (buffer, tile)
-  constexpr int B_CE = B_CF + 1, B_DR = B_CE + 1;
+  constexpr int B_CE = B_CF + 1, B_IF = B_CE + 1, B_IE = B_IF + C::QD, B_DR = B_IE + C::QD;
   constexpr int N_BARS = B_DR + 1;
-  static_assert(8 * N_BARS + 8 <= 256, "barrier region");
+  static_assert(8 * N_BARS + 8 <= C::MISC_QUEUE, "barrier region");
   const uint32_t bar0 = sbase + C::SMEM_MISC;
 #define BAR(i) (bar0 + 8u * static_cast<uint32_t>(i))
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC + 8 * N_BARS);
@@ -329,6 +338,10 @@ __global__ void __launch_bounds__(640, 1)
     }
     mbar_init(BAR(B_CF), 4 * (4 - C::SUBS));  // warps of the buffers after the first
     mbar_init(BAR(B_CE), 4 * C::SUBS);        // warps of the first buffer
+    for (int s = 0; s < C::QD; ++s) {
+      mbar_init(BAR(B_IF + s), 1);
+      mbar_init(BAR(B_IE + s), 19);  // one elected lane of every other warp
+    }
     mbar_init(BAR(B_DR), 1);
     *abort_flag = 0;
     fence_mbar_init();
@@ -343,6 +356,18 @@ __global__ void __launch_bounds__(640, 1)
   const uint32_t tmem = *tmem_slot;
   bool ok = true;
   pdl_trigger();
+  volatile WeightsEntry* queue = reinterpret_cast<volatile WeightsEntry*>(
+      smem + C::SMEM_MISC + C::MISC_QUEUE);
+  static_assert(sizeof(WeightsEntry) <= 64, "queue entry");
+  // Range `i` of the CTA, once it is there (null: the end of the list, or a wait that gave up); for
+  // one lane, or with `warp_wide` for a whole warp alike.
+  auto range = [&](uint32_t i, bool warp_wide) {
+    ok = mbar_wait(BAR(B_IF + i % C::QD), (i / C::QD) & 1u, abort_flag, tmo, ecode | 11);
+    if (warp_wide) ok = __all_sync(0xffffffffu, ok);
+    volatile WeightsEntry* e = reinterpret_cast<volatile WeightsEntry*>(
+        reinterpret_cast<volatile uint8_t*>(queue) + 64u * (i % C::QD));
+    return ok && e->flags != 0 ? e : nullptr;
+  };
 
   if (warp >= 16)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_OTHER));
@@ -350,12 +375,12 @@ __global__ void __launch_bounds__(640, 1)
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_SUM));
   if (warp == 17) {
     // ---------------------------------------------------------------- TMA producer
-    Walk w;
-    w.init(p, gridDim.x, blockIdx.x);
     if (lane == 0) {
-      WeightsFrag f;
       uint32_t n_frag = 0, k = 0;
-      while (ok && w.next(p, f)) {
+      while (volatile WeightsEntry* e = range(n_frag, false)) {
+        const int g = e->g, q_row = e->q0 + e->qbeg, k_row = e->k0 + e->j0, nt = e->nt;
+        const int s0 = e->s0, s1 = e->s1;
+        mbar_arrive(BAR(B_IE + n_frag % C::QD));
         const uint32_t kb = n_frag % C::NK;
         ok = mbar_wait(BAR(B_KE + kb), ((n_frag / C::NK) & 1u) ^ 1u, abort_flag, tmo, ecode | 1);
         if (!ok) break;
@@ -365,10 +390,10 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
           for (int a = 0; a < C::ATOMS; ++a)
             tma_load_3d(sbase + C::SMEM_K + (kb * C::SUBS + h) * C::TILE_BYTES + a * C::ATOM_BYTES,
-                        &tm_k, BAR(B_KF + kb), a * 64, f.g, f.k0 + f.j0 + h * 128);
+                        &tm_k, BAR(B_KF + kb), a * 64, g, k_row + h * 128);
         ++n_frag;
-        int hb = f.s0 / f.nt, t = f.s0 - hb * f.nt;
-        for (int st = f.s0; st < f.s1; ++st, ++k) {
+        int hb = s0 / nt, t = s0 - hb * nt;
+        for (int st = s0; st < s1; ++st, ++k) {
           const uint32_t s = k % C::NQ;
           ok = mbar_wait(BAR(B_QE + s), ((k / C::NQ) & 1u) ^ 1u, abort_flag, tmo, ecode | 2);
           if (!ok) break;
@@ -376,13 +401,14 @@ __global__ void __launch_bounds__(640, 1)
 #pragma unroll
           for (int a = 0; a < C::ATOMS; ++a)
             tma_load_3d(sbase + C::SMEM_Q + s * C::TILE_BYTES + a * C::ATOM_BYTES, &tm_q,
-                        BAR(B_QF + s), a * 64, f.g * p.R + (hb << p.log2_p),
-                        f.q0 + f.qbeg + t * (128 >> p.log2_p));
-          if (++t == f.nt) {
+                        BAR(B_QF + s), a * 64, g * p.R + (hb << p.log2_p),
+                        q_row + t * (128 >> p.log2_p));
+          if (++t == nt) {
             t = 0;
             ++hb;
           }
         }
+        if (!ok) break;
       }
       if (!ok) {
         // Let the loads already issued land before the CTA's shared memory goes away.
@@ -400,18 +426,17 @@ __global__ void __launch_bounds__(640, 1)
     __syncwarp();
   } else if (warp == 16) {
     // ---------------------------------------------------------------- tcgen05 issuer
-    Walk w;
-    w.init(p, gridDim.x, blockIdx.x);
     if (lane == 0) {
       constexpr uint32_t IDESC = umma_idesc_f16(BF16, 128, 128, false, false);
-      WeightsFrag f;
       uint32_t n_frag = 0, k = 0;
-      while (ok && w.next(p, f)) {
+      while (volatile WeightsEntry* e = range(n_frag, false)) {
+        const int s0 = e->s0, s1 = e->s1;
+        mbar_arrive(BAR(B_IE + n_frag % C::QD));
         const uint32_t kb = n_frag % C::NK;
         ok = mbar_wait(BAR(B_KF + kb), (n_frag / C::NK) & 1u, abort_flag, tmo, ecode | 3);
         if (!ok) break;
         ++n_frag;
-        for (int st = f.s0; st < f.s1; ++st, ++k) {
+        for (int st = s0; st < s1; ++st, ++k) {
           const uint32_t s = k % C::NQ, b = k % C::NBUF;
           ok = mbar_wait(BAR(B_QF + s), (k / C::NQ) & 1u, abort_flag, tmo, ecode | 4);
           if (!ok) break;
@@ -433,8 +458,9 @@ __global__ void __launch_bounds__(640, 1)
           }
           if (!ok) break;
           mma_commit(BAR(B_QE + s));
-          if (st == f.s1 - 1) mma_commit(BAR(B_KE + kb));
+          if (st == s1 - 1) mma_commit(BAR(B_KE + kb));
         }
+        if (!ok) break;
       }
       // Every MMA issued so far must finish before TMEM is released.
       mma_commit(BAR(B_DR));
@@ -446,28 +472,30 @@ __global__ void __launch_bounds__(640, 1)
     // ---------------------------------------------------------------- column terms
     //   nl[c] = -lse2 (causal ALiBi: - slope2 (p_c - j0) as well: with the key's own + slope2 key the
     //   terms stay small where weights are not), sl[c] = slope2, ps[c] = p_c - j0.
-    Walk w;
-    w.init(p, gridDim.x, blockIdx.x);
-    WeightsFrag f;
-    uint32_t k = 0;
-    while (ok && w.next(p, f)) {
-      int hb = f.s0 / f.nt, t = f.s0 - hb * f.nt;
-      for (int st = f.s0; st < f.s1; ++st, ++k) {
+    uint32_t n_frag = 0, k = 0;
+    while (volatile WeightsEntry* e = range(n_frag, true)) {
+      const int g = e->g, q0 = e->q0, lq = e->lq, qbeg = e->qbeg, nt = e->nt;
+      const int s0 = e->s0, s1 = e->s1, pos0 = e->lk - lq - e->j0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(BAR(B_IE + n_frag % C::QD));
+      ++n_frag;
+      int hb = s0 / nt, t = s0 - hb * nt;
+      for (int st = s0; st < s1; ++st, ++k) {
         const uint32_t b = k % C::NBUF;
         float nl[4], sl[4], ps[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int c = u * 32 + lane;
-          const int i = f.qbeg + t * (128 >> p.log2_p) + (c >> p.log2_p);
-          const int head = f.g * p.R + (hb << p.log2_p) + (c & ((1 << p.log2_p) - 1));
+          const int i = qbeg + t * (128 >> p.log2_p) + (c >> p.log2_p);
+          const int head = g * p.R + (hb << p.log2_p) + (c & ((1 << p.log2_p) - 1));
           nl[u] = -INFINITY;
           sl[u] = ps[u] = 0.f;
-          if (i < f.lq) {
-            nl[u] = -LOG2E * __ldg(p.lse + static_cast<size_t>(head) * p.total_q + f.q0 + i);
+          if (i < lq) {
+            nl[u] = -LOG2E * __ldg(p.lse + static_cast<size_t>(head) * p.total_q + q0 + i);
             if (nl[u] == INFINITY) nl[u] = -INFINITY;  // (a row that attends to nothing)
             if constexpr (ALIBI) {
               sl[u] = __ldg(p.slopes + head) * LOG2E;
-              ps[u] = static_cast<float>(i + f.lk - f.lq - f.j0);
+              ps[u] = static_cast<float>(i + pos0);
               if (CAUSAL) nl[u] -= sl[u] * ps[u];
             }
           }
@@ -487,12 +515,44 @@ __global__ void __launch_bounds__(640, 1)
         }
         __syncwarp();
         if (lane < C::SUBS) mbar_arrive(BAR(B_SF + b * C::SUBS + lane));
-        if (++t == f.nt) {
+        if (++t == nt) {
           t = 0;
           ++hb;
         }
       }
+      if (!ok) break;
     }
+  } else if (warp == 19) {
+    // ---------------------------------------------------------------- schedule
+    WeightsWalk<C::KT, CAUSAL> w;
+    w.init(p, gridDim.x, blockIdx.x);
+    if (lane == 0) {
+      WeightsFrag f;
+      for (uint32_t i = 0;; ++i) {
+        if (!mbar_wait(BAR(B_IE + i % C::QD), ((i / C::QD) & 1u) ^ 1u, abort_flag, tmo, ecode | 12))
+          break;
+        volatile WeightsEntry* e = reinterpret_cast<volatile WeightsEntry*>(
+            reinterpret_cast<volatile uint8_t*>(queue) + 64u * (i % C::QD));
+        const bool more = w.next(p, f);
+        if (more) {
+          e->seg = f.seg;
+          e->g = f.g;
+          e->q0 = f.q0;
+          e->lq = f.lq;
+          e->k0 = f.k0;
+          e->lk = f.lk;
+          e->j0 = f.j0;
+          e->qbeg = f.qbeg;
+          e->nt = f.nt;
+          e->s0 = f.s0;
+          e->s1 = f.s1;
+        }
+        e->flags = more ? WF_LIVE | (f.whole ? WF_WHOLE : 0) | (f.first ? WF_FIRST : 0) : 0;
+        mbar_arrive(BAR(B_IF + i % C::QD));
+        if (!more) break;
+      }
+    }
+    __syncwarp();
   } else if (warp < 16) {
     // ---------------------------------------------------------------- sums (thread = key)
     const int wg = warp >> 2;
@@ -507,21 +567,22 @@ __global__ void __launch_bounds__(640, 1)
     const uint64_t c1x2 = f2_pack(p.c1, p.c1);
     const float key = static_cast<float>(h * 128 + r);
     float* sums = reinterpret_cast<float*>(smem + C::SMEM_SUM);
-    Walk w;
-    w.init(p, gridDim.x, blockIdx.x);
-    WeightsFrag f;
-    uint32_t n_frag = 0, phase = 0;
+    uint32_t n_frag = 0, n_join = 0, phase = 0;
     int ahead = buf;  // steps until this warpgroup's next one
-    while (ok && w.next(p, f)) {
+    while (volatile WeightsEntry* e = range(n_frag, true)) {
+      const uint32_t bar_ie = BAR(B_IE + n_frag % C::QD);
+      ++n_frag;
       float sum = 0.f, comp = 0.f;  // running sum and what it lost
-      const int j = f.j0 + h * 128 - (f.lk - f.lq) - f.qbeg;  // first key, counted in queries
-      const int left = f.lq - f.qbeg;
-      int t = (f.s0 + ahead) % f.nt;
-      int n = f.s1 - f.s0 - ahead;
+      const int s0 = e->s0, s1 = e->s1, nt = e->nt, qbeg = e->qbeg;
+      const int j = e->j0 + h * 128 - (e->lk - e->lq) - qbeg;  // first key, counted in queries
+      const int left = e->lq - qbeg;
+      int t = (s0 + ahead) % nt;
+      int n = s1 - s0 - ahead;
+      const bool mine = n > 0;
       for (; n > 0; n -= C::NBUF) {
         const int qi = t << (7 - p.log2_p);  // first query of the tile
         t += C::NBUF;
-        while (t >= f.nt) t -= f.nt;
+        while (t >= nt) t -= nt;
         // Columns [lo, hi) count for this key; every key of the tile sees all 128 off the edges.
         const int hi = (left - qi) << p.log2_p;
         const bool edge = hi < 128 || (CAUSAL && qi < j + 127);
@@ -573,29 +634,46 @@ __global__ void __launch_bounds__(640, 1)
       }
       ahead = -n;
       if (!ok) break;
-      // ---- the warpgroups' sums join, and the item's (or the range's) are written
-      if (buf > 0) {
-        ok = mbar_wait(BAR(B_CE), (n_frag & 1u) ^ 1u, abort_flag, tmo, ecode | 9);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        sums[(wg - C::SUBS) * 128 + r] = sum;
+      // ---- the warpgroups' sums join, and the item's (or the range's) are written. A range of one
+      // step is its warpgroups' alone: the others have gone on.
+      const bool solo = s1 - s0 == 1;
+      if (solo && !mine) {
         __syncwarp();
-        if (lane == 0) mbar_arrive(BAR(B_CF));
-      } else {
-        ok = mbar_wait(BAR(B_CF), n_frag & 1u, abort_flag, tmo, ecode | 10);
+        if (lane == 0) mbar_arrive(bar_ie);
+        continue;
+      }
+      if (!solo) {
+        if (buf > 0) {
+          ok = mbar_wait(BAR(B_CE), (n_join & 1u) ^ 1u, abort_flag, tmo, ecode | 9);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          sums[(wg - C::SUBS) * 128 + r] = sum;
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(BAR(B_CF));
+            mbar_arrive(bar_ie);
+          }
+          ++n_join;
+          continue;
+        }
+        ok = mbar_wait(BAR(B_CF), n_join & 1u, abort_flag, tmo, ecode | 10);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
 #pragma unroll
         for (int q = 1; q < C::NBUF; ++q) sum += sums[(q * C::SUBS + h - C::SUBS) * 128 + r];
         __syncwarp();
         if (lane == 0) mbar_arrive(BAR(B_CE));
-        const int row = h * 128 + r;
-        if (!f.whole)
-          p.ws[(2 * static_cast<size_t>(blockIdx.x) + (f.first ? 0 : 1)) * C::KT + row] = sum;
-        else if (f.j0 + row < f.lk && f.j0 + row < p.w_stride)
-          p.weights[(static_cast<size_t>(f.seg) * p.hkv + f.g) * p.w_stride + f.j0 + row] = sum;
+        ++n_join;
       }
-      ++n_frag;
+      const int row = h * 128 + r;
+      const int flags = e->flags, key0 = e->j0 + row, lk = e->lk;
+      const size_t out = (static_cast<size_t>(e->seg) * p.hkv + e->g) * p.w_stride + key0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar_ie);
+      if (!(flags & WF_WHOLE))
+        p.ws[(2 * static_cast<size_t>(blockIdx.x) + (flags & WF_FIRST ? 0 : 1)) * C::KT + row] = sum;
+      else if (key0 < lk && key0 < p.w_stride)
+        p.weights[out] = sum;
     }
   }
 #undef BAR
