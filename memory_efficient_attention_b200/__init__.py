@@ -802,6 +802,8 @@ def decode_tree_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     out = _output("out", out, (tq, hq, d), q.dtype, idx)
     lse = _output("lse", lse, (hq, tq), torch.float32, idx)
     slopes = _slopes_for(alibi_slopes, hq, idx)
+    if tq == 0:
+        return out, lse
     _launch(idx, "mea_decode_tree", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             table.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), mask.data_ptr(), out.data_ptr(),
             lse.data_ptr(), n, tq, int(max_seqlen_q), int(max_seqlen_k), mask.size(1), nb, bs,

@@ -442,7 +442,8 @@ __global__ void __launch_bounds__(160, 1)
           const int e = e_next;
           e_next = entry(t + 1);
           // (an entry past the request's blocks names no key; its product must not wrap)
-          const bool in = e >= 0 && e < (L + p.block_size - 1) / p.block_size;
+          const bool in =
+              e >= 0 && e < min((L + p.block_size - 1) / p.block_size, p.max_blocks);
           first = in ? e * p.block_size + first % p.block_size : 0;
           live = in ? L - first : 0;
         }

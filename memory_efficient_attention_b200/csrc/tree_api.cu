@@ -315,10 +315,10 @@ int mea_attention_weights(const void* q, const void* k, const float* lse,
   p.c1 = scale * 1.4426950408889634f;
   p.timeout_ns = g_timeout_ns.load();
   CUtensorMap tq, tk;
-  // (without queries nothing of the q map is read: any address of the right alignment serves)
-  const uint64_t q_rows = total_q > 0 ? static_cast<uint64_t>(total_q) : 1;
-  if (!encode_3d(&tq, total_q > 0 ? q : k, dtype, head_dim, total_q > 0 ? n_heads_q : n_heads_kv,
-                 q_rows, 64, total_q > 0 ? 1u << log2_p : 1u, 128u >> log2_p) ||
+  // (without queries the q map is not used)
+  if (!(total_q > 0 ? encode_3d(&tq, q, dtype, head_dim, n_heads_q, total_q, 64, 1u << log2_p,
+                                128u >> log2_p)
+                    : encode_3d(&tq, k, dtype, head_dim, n_heads_kv, total_k, 64, 1, 128)) ||
       !encode_3d(&tk, k, dtype, head_dim, n_heads_kv, total_k, 64, 1, 128))
     return MEA_ERR_CUDA;
   // No more CTAs than steps.

@@ -380,6 +380,7 @@ __global__ void __launch_bounds__(640, 1)
       while (volatile WeightsEntry* e = range(n_frag, false)) {
         const int g = e->g, q_row = e->q0 + e->qbeg, k_row = e->k0 + e->j0, nt = e->nt;
         const int s0 = e->s0, s1 = e->s1;
+        const bool none = e->qbeg >= e->lq;  // no query: the step's columns may hold anything
         mbar_arrive(BAR(B_IE + n_frag % C::QD));
         const uint32_t kb = n_frag % C::NK;
         ok = mbar_wait(BAR(B_KE + kb), ((n_frag / C::NK) & 1u) ^ 1u, abort_flag, tmo, ecode | 1);
@@ -397,6 +398,10 @@ __global__ void __launch_bounds__(640, 1)
           const uint32_t s = k % C::NQ;
           ok = mbar_wait(BAR(B_QE + s), ((k / C::NQ) & 1u) ^ 1u, abort_flag, tmo, ecode | 2);
           if (!ok) break;
+          if (none) {
+            mbar_arrive(BAR(B_QF + s));
+            continue;
+          }
           mbar_arrive_expect_tx(BAR(B_QF + s), C::TILE_BYTES);
 #pragma unroll
           for (int a = 0; a < C::ATOMS; ++a)
