@@ -825,18 +825,33 @@ __global__ void __launch_bounds__(256)
   if (t0 >= L) return;
   __shared__ int s_start;
   __shared__ float s_lse[R_MAX];
-  const int n = dec_nchunks(p.cu_k, b, p.chunk);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int st = dec_chunk_start(p.cu_k, b, p.chunk);
+  // (never past the workspace, should the key counts exceed the bound they were sized by)
+  const int n = min(dec_nchunks(p.cu_k, b, p.chunk), p.n_slots - st);
+  if (L > n * static_cast<long long>(p.chunk)) L = max(n, 0) * p.chunk;
   if (threadIdx.x == 0) s_start = st;
   const float* prev = p.prev ? p.prev + (static_cast<size_t>(b) * gridDim.y + g) * p.w_stride
                              : nullptr;
   float* out = p.weights + (static_cast<size_t>(b) * gridDim.y + g) * p.w_stride;
-  float w[4];
+  // Four consecutive keys, which lie in one chunk (chunks are multiples of 64 keys): 16-byte loads of
+  // their scores.
+  const int t = t0 + 4 * threadIdx.x;
+  const bool row16 = (reinterpret_cast<uintptr_t>(out) & 15u) == 0 &&
+                     (reinterpret_cast<uintptr_t>(prev) & 15u) == 0;
+  float w[4] = {0.f, 0.f, 0.f, 0.f};
+  if (prev) {
+    if (row16 && t + 3 < L) {
+      const float4 v = *reinterpret_cast<const float4*>(prev + t);
+      w[0] = v.x;
+      w[1] = v.y;
+      w[2] = v.z;
+      w[3] = v.w;
+    } else {
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int t = t0 + u * 256 + threadIdx.x;
-    w[u] = (prev && t < L) ? prev[t] : 0.f;
+      for (int u = 0; u < 4; ++u)
+        if (t + u < L) w[u] = prev[t + u];
+    }
   }
   for (int rb = 0; rb < p.R; rb += R_MAX) {  // heads of the group, R_MAX at a time
     const int rn = min(R_MAX, p.R - rb);
@@ -856,25 +871,30 @@ __global__ void __launch_bounds__(256)
       if (lane == 0) s_lse[rr] = z > 0.f ? (m + __logf(z)) * LOG2E : INFINITY;
     }
     __syncthreads();
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int t = t0 + u * 256 + threadIdx.x;
-      if (t < L) {
-        const int c = t / p.chunk;
-        const float* sc = p.ws_s +
-                          (static_cast<size_t>(s_start + c) * p.hq + g * p.R + rb) * p.chunk +
-                          (t - c * p.chunk);
+    if (t < L) {
+      const int c = t / p.chunk;
+      const float* sc = p.ws_s +
+                        (static_cast<size_t>(s_start + c) * p.hq + g * p.R + rb) * p.chunk +
+                        (t - c * p.chunk);
 #pragma unroll 8
-        for (int rr = 0; rr < rn; ++rr)
-          w[u] += ex2_approx(__ldcs(sc + static_cast<size_t>(rr) * p.chunk) - s_lse[rr]);
+      for (int rr = 0; rr < rn; ++rr) {
+        const float4 x =
+            __ldcs(reinterpret_cast<const float4*>(sc + static_cast<size_t>(rr) * p.chunk));
+        const float z = s_lse[rr];
+        w[0] += ex2_approx(x.x - z);
+        w[1] += ex2_approx(x.y - z);
+        w[2] += ex2_approx(x.z - z);
+        w[3] += ex2_approx(x.w - z);
       }
     }
     __syncthreads();
   }
+  if (row16 && t + 3 < L) {
+    *reinterpret_cast<float4*>(out + t) = make_float4(w[0], w[1], w[2], w[3]);
+  } else {
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int t = t0 + u * 256 + threadIdx.x;
-    if (t < L) out[t] = w[u];
+    for (int u = 0; u < 4; ++u)
+      if (t + u < L) out[t + u] = w[u];
   }
 }
 
