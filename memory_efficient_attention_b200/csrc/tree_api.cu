@@ -40,7 +40,7 @@ int launch_tree(const CUtensorMap& tk, const CUtensorMap& tv, const mea::TreePar
   if (cudaGetLastError() != cudaSuccess) return MEA_ERR_CUDA;
   if (grid > 1 && launch_dependent(mea::mea_tree_merge_kernel<D, BF16>,
                                    dim3(static_cast<unsigned>(grid - 1),
-                                        static_cast<unsigned>((rows + 7) / 8)),
+                                        static_cast<unsigned>((rows + 15) / 16)),
                                    256, 0, s,
                                    p, grid) != cudaSuccess)
     return MEA_ERR_CUDA;

@@ -808,18 +808,24 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(256) mea_tree_merge_kernel(const TreeParams p, int grid) {
   using C = TreeCfg<D>;
   constexpr int ROWS = C::ROWS;
-  pdl_wait();
   const long long total = tree_total<ROWS>(p);
   const long long per = div_nn(total + grid - 1, grid);
   const long long pos = per * (blockIdx.x + 1);
-  if (pos >= total) return;
-  long long base = 0;
-  const int b = tree_find<ROWS>(p, pos, base);
-  const TreeSeq s = tree_seq<ROWS>(p, b);
-  const int item = static_cast<int>(div_nn(pos - base, s.tiles));
-  const long long i0 = base + static_cast<long long>(item) * s.tiles;  // the item's tiles
-  const long long i1 = i0 + s.tiles;
-  if (i0 == pos || i0 < pos - per) return;  // not crossed here, or first crossed earlier
+  long long base = 0, i0 = 0, i1 = 0;  // the item's tiles [i0, i1)
+  TreeSeq s{};
+  int item = 0;
+  bool mine = pos < total;
+  if (mine) {
+    s = tree_seq<ROWS>(p, tree_find<ROWS>(p, pos, base));
+    item = static_cast<int>(div_nn(pos - base, s.tiles));
+    i0 = base + static_cast<long long>(item) * s.tiles;
+    i1 = i0 + s.tiles;
+    mine = i0 < pos && i0 >= pos - per;  // crossed here, and not earlier
+  }
+  // Up to here nothing that the first kernel writes was read. (Every CTA waits, also those that then
+  // have nothing to do: this grid must not end before the first one.)
+  pdl_wait();
+  if (!mine) return;
   const int c0 = blockIdx.x;
   const int c1 = static_cast<int>(div_nn(i1 - 1, per));  // last CTA with a part
   const int g = item / s.parts;
