@@ -1,6 +1,6 @@
 // host_util.h — host-side helpers shared by the translation units of libmea: device attributes,
 // TMA descriptor encoding (with its cache), one-time kernel attributes and the split-KV layout.
-// Inline, so that both units share one timeout, one device table and one descriptor cache.
+// Inline, so that all units share one timeout, one device table and one descriptor cache.
 #pragma once
 
 #include <cudaTypedefs.h>

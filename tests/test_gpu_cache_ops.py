@@ -196,6 +196,8 @@ def test_decode_weights(lens, hq, hkv, d, dtype, bs, alibi, split, prev):
     ([700, 31, 32], [700, 31, 32], 8, 2, 128, BF, True, True, 32),
     ([700, 500], [700, 500], 8, 4, 256, BF, True, False, 129),
     ([300, 0], [300, 60], 4, 1, 256, FP, False, False, 1),
+    ([260], [260], 6, 2, 136, BF, True, False, 0),
+    ([300, 700], [300, 700], 64, 1, 64, BF, True, True, 3),  # 64 heads in a tile
 ])
 def test_prompt_weights(lens_q, lens_k, hq, hkv, d, dtype, causal, alibi, last):
     q, k, v = make_qkv(lens_q, lens_k, hq, hkv, d, dtype, 61)
@@ -314,6 +316,7 @@ def random_tree(n, gen):
     ([256] * 70, [4] * 70, 8, 2, 40, FP, 64, True),
     ([3000, 1700, 129, 128], [16, 2, 1, 16], 16, 2, 128, BF, 16, True),  # one sub-tile's rows
     ([4000, 300] * 30, [40, 3] * 30, 16, 2, 64, FP, 32, False),  # one and two sub-tiles in turn
+    ([500, 64], [11, 2], 4, 2, 136, BF, 32, False),              # a head dim that ends in a box
 ])
 def test_tree(lens, nq, hq, hkv, d, dtype, bs, alibi):
     c = ref.Cache(lens, hq, hkv, d, dtype, bs, 81)
