@@ -363,7 +363,8 @@ int mea_attention_weights(const void* q, const void* k, const float* lse,
  *   out_table    DEVICE int32 [n_seqs, max_out_blocks], max_out_blocks * block_size >=
  *                min(n_keep, max_seqlen_k): the new blocks, in the caches out_k_cache, out_v_cache
  *                DEVICE [num_out_blocks, block_size, n_heads_kv, D]. These may be k_cache and v_cache
- *                themselves, as long as no new block is one that a request still reads from.
+ *                themselves, as long as no new block is one that a request still reads from. No
+ *                block is named twice.
  *                Slots past the kept keys are left as they were.
  *   kept         DEVICE int32 [n_seqs, n_heads_kv, n_keep]: the kept keys' indices, ascending, then -1.
  *   out_weights  DEVICE fp32 [n_seqs, n_heads_kv, n_keep]: the kept keys' weights, then 0. Not weights.

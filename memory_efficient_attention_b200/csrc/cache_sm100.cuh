@@ -343,9 +343,10 @@ __device__ __forceinline__ void compact_selected(Get get, Put put, int n, uint32
 // Bound by reading the ranges (4 D bytes a block and head); in 64 bits throughout, the conversions and
 // products took three times as long as that. So the scores are first computed on the tensor cores
 // (mma.sync, 16 blocks a tile, w = (down, up) as three 16-bit pieces in three of the eight columns,
-// fp32 sums), which is off by at most delta = 2^-16 sum|w| max|range| (48 products' sums of 2^-23 at
-// most each, with room), and the blocks within 2 delta of the cut, one or two as a rule, are scored
-// again in 64 bits: a block further above (below) the cut than that is above (below) it in 64 bits too.
+// fp32 sums), which is off by at most delta = CHUNKS 2^-17 sum|w| max|range| (2 CHUNKS instructions, each of
+// which adds 17 terms aligned to the largest with an error of 2^-23 of it at most), and the blocks
+// within 2 delta of the cut, a few as a rule, are scored again in 64 bits: a block further above (below)
+// the cut than that is above (below) it in 64 bits too.
 // A cluster of CTAs serves one (request, KV head): each CTA's warps score a share of its blocks and
 // leave the rank keys in the first CTA's shared memory, which then selects.
 // ------------------------------------------------------------------------------------------
@@ -515,25 +516,33 @@ __global__ void __launch_bounds__(kSelThreads, CHUNKS == 16 ? 1 : 2)
     __syncthreads();
   if (cr != 0) return;
   auto get = [&](int i) { return s_keys[i]; };
-  auto put = [&](int at, int i, uint32_t) { out[at] = i; };
+  auto put = [&](int at, int i, uint32_t) {
+    if (at < p.n_select) out[at] = i;
+  };
   int ties = 0;
   uint32_t T = radix_select<kSelThreads>(get, nblk, p.n_select, s_sc, ties);
   if (T != kRankAlways) {
     // delta, in every warp
-    float most_all = 0.f, sum_w = 0.f;
+    float most_all = 0.f, sum_w = 0.f, most_w = 0.f;
     for (int i = lane; i < cs * (kSelThreads / 32); i += 32) most_all = max_nan(most_all, s_most[i]);
-    for (int d = lane; d < 2 * p.dh; d += 32) sum_w += fabsf(static_cast<float>(s_w[d]));
+    for (int d = lane; d < 2 * p.dh; d += 32) {
+      const float x = fabsf(static_cast<float>(s_w[d]));
+      sum_w += x;
+      most_w = max_nan(most_w, x);
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
       most_all = max_nan(most_all, __shfl_xor_sync(0xffffffffu, most_all, off));
       sum_w += __shfl_xor_sync(0xffffffffu, sum_w, off);
+      most_w = max_nan(most_w, __shfl_xor_sync(0xffffffffu, most_w, off));
     }
-    // (the last term: third pieces below a half's smallest step; a NaN or an infinity in the ranges
-    // or the queries makes delta one, and every block is scored again)
-    const float delta = 0x1p-16f * sum_w * most_all + 0x1p-15f * most_all;
+    // (the last term: third pieces below a half's smallest step)
+    const float delta = CHUNKS * 0x1p-17f * sum_w * most_all + 0x1p-15f * most_all;
     const float cut = rank_value(T);
     const float above = cut + 2.f * delta, below = cut - 2.f * delta;
-    const bool sane = delta < 0x1p120f;
+    // Otherwise every block is scored again: a NaN or an infinity somewhere, sums that fp32 might not
+    // hold, queries' sums that a half does not.
+    const bool sane = delta < 0x1p100f && (BF16 || most_w < 65504.f);
     // Keys become "in", 1 (out) or 2 (to be scored again).
     int n_in = 0, n_again = 0;
     for (int i = tid; i < nblk; i += kSelThreads) {

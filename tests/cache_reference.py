@@ -128,7 +128,9 @@ def choose(c, q, bounds, n_select, n_first, n_last):
         for g in range(c.hkv):
             x = q[b, g * r:(g + 1) * r].double()
             lo, hi = bounds[c.table[b, :nblk].long(), g].double().unbind(1)
-            score = (torch.maximum(x[:, None] * lo, x[:, None] * hi)).sum((0, 2)).float()
+            # (for ranges with lo <= hi: the sum over heads and columns of max(x lo, x hi))
+            up, down = x.clamp_min(0).sum(0), x.clamp_max(0).sum(0)
+            score = (hi * up + lo * down).sum(1).float()
             order = sorted(range(nblk), key=lambda j: (
                 not (j < n_first or j >= nblk - n_last),
                 0.0 if (j < n_first or j >= nblk - n_last) else -float(score[j]), j))

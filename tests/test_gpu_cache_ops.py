@@ -98,6 +98,39 @@ def test_select_blocks_ties_and_nan():
     assert got.cpu()[0, 0].tolist() == [25, 30, 39]
 
 
+@pytest.mark.parametrize("dtype,factor", [(BF, 1e30), (BF, 1e-30), (FP, 3e4), (FP, 1e-6)])
+def test_select_blocks_extreme_queries(dtype, factor):
+    """Queries whose sums leave the range of fp32 products, or of 16 bits, change nothing in the choice's
+    definition."""
+    c = ref.Cache([900, 3000], 8, 2, 64, dtype, 16, 23)
+    q = (randn((2, 8, 64), 24, torch.float32) * factor).clamp(-6e4, 6e4).to(dtype) \
+        if dtype == FP else (randn((2, 8, 64), 24, torch.float32) * factor).to(dtype)
+    bounds, _ = ref.block_bounds(c)
+    if factor > 1e20:
+        bounds = (bounds.float() * 1e8).to(dtype)
+    _, _, table, cu = c.gpu()
+    got = mea.select_blocks(q.cuda(), bounds.cuda(), table, cu, c.max, 16, 21).cpu()
+    want = ref.choose(c, q, bounds, 21, 1, 1)
+    for b in range(2):
+        for g in range(2):
+            assert got[b, g].tolist() == want[b][g]
+
+
+def test_select_blocks_many_near_the_cut():
+    """More blocks within the first scores' error than a list holds: all are decided in 64 bits."""
+    c = ref.Cache([16 * 300], 4, 1, 128, BF, 16, 25)
+    q = randn((1, 4, 128), 26, BF)
+    bounds = randn((1, 1, 2, 128), 27, BF).expand(c.num_blocks, -1, -1, -1).clone()
+    # Blocks differ in one column, by one rounding step of a value that hardly counts.
+    pos = torch.randperm(300, generator=torch.Generator().manual_seed(28))
+    for j in range(300):
+        bounds[int(c.table[0, j]), 0, 1, 5] = 2.0 ** -12 * (1 + int(pos[j]) % 100 / 128)
+    _, _, table, cu = c.gpu()
+    got = mea.select_blocks(q.cuda(), bounds.cuda(), table, cu, c.max, 16, 50, n_first=0,
+                            n_last=2).cpu()
+    assert got[0, 0].tolist() == ref.choose(c, q, bounds, 50, 0, 2)[0][0]
+
+
 # --------------------------------------------------------------------- decode over chosen blocks
 @pytest.mark.parametrize("lens,hq,hkv,d,dtype,bs,n_select,alibi", [
     ([1], 1, 1, 8, FP, 16, 1, False),
