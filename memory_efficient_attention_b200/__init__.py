@@ -405,6 +405,7 @@ def decode_splitkv_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _cur_device = torch._C._cuda_getDevice
 _INV_SQRT: dict = {}  # head dim -> 1 / sqrt
+_DTYPE_CODES = {torch.float16: _lib.MEA_F16, torch.bfloat16: _lib.MEA_BF16}
 
 
 def _gpu_index(t: torch.Tensor) -> int:
@@ -427,8 +428,9 @@ def _check_prefix(name: str, t: torch.Tensor, n: int, idx: int) -> torch.Tensor:
     """An int32 ``[n]`` tensor on GPU ``idx`` (made contiguous)."""
     if t.dtype is not torch.int32 or t.dim() != 1 or t.numel() != n:
         raise MeaError(_lib.MEA_ERR_SHAPE, f"{name} must be int32 [{n}]")
-    _same_gpu(name, t, idx)
-    return _dense(t)
+    if t.get_device() != idx:
+        _same_gpu(name, t, idx)
+    return t if t.is_contiguous() else t.contiguous()
 
 
 def _check_paged(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor],
@@ -438,7 +440,9 @@ def _check_paged(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor],
     on one GPU, and, with ``q [rows, Hq, D]``, of its dtype and head dim. (A cache is never copied
     here to make it contiguous.) Returns the GPU's index, the cache's shape and dtype code, the
     block table and the prefix sums (contiguous)."""
-    idx = _gpu_index(k_cache)
+    idx = k_cache.get_device()
+    if idx < 0:
+        _gpu_index(k_cache)
     shape = k_cache.shape
     if len(shape) != 4 or not k_cache.is_contiguous():
         raise MeaError(_lib.MEA_ERR_SHAPE,
@@ -449,18 +453,27 @@ def _check_paged(k_cache: torch.Tensor, v_cache: Optional[torch.Tensor],
             raise MeaError(_lib.MEA_ERR_SHAPE, "k_cache and v_cache must be alike and contiguous")
         if v_cache.dtype is not dtype:
             raise MeaError(_lib.MEA_ERR_DTYPE, "k_cache and v_cache must share one dtype")
-        _same_gpu("v_cache", v_cache, idx)
+        if v_cache.get_device() != idx:
+            _same_gpu("v_cache", v_cache, idx)
     if q is not None:
         if q.dim() != 3 or q.size(2) != shape[3]:
             raise MeaError(_lib.MEA_ERR_SHAPE, "q must be [rows, Hq, D] with the cache's D")
         if q.dtype is not dtype:
             raise MeaError(_lib.MEA_ERR_DTYPE, "q and the cache must share one dtype")
-        _same_gpu("q", q, idx)
+        if q.get_device() != idx:
+            _same_gpu("q", q, idx)
     if block_table.dim() != 2 or block_table.dtype is not torch.int32:
         raise MeaError(_lib.MEA_ERR_SHAPE, "block_table must be int32 [n_seqs, max_blocks]")
-    _same_gpu("block_table", block_table, idx)
-    cu = _check_prefix("cu_seqlens_k", cu_seqlens_k, block_table.size(0) + 1, idx)
-    return idx, shape, _dtype_code(dtype), _dense(block_table), cu
+    if block_table.get_device() != idx:
+        _same_gpu("block_table", block_table, idx)
+    if cu_seqlens_k.dtype is not torch.int32 or cu_seqlens_k.dim() != 1 \
+            or cu_seqlens_k.numel() != block_table.size(0) + 1 \
+            or cu_seqlens_k.get_device() != idx:
+        _check_prefix("cu_seqlens_k", cu_seqlens_k, block_table.size(0) + 1, idx)
+    code = _DTYPE_CODES.get(dtype)
+    return (idx, shape, _dtype_code(dtype) if code is None else code,
+            block_table if block_table.is_contiguous() else block_table.contiguous(),
+            cu_seqlens_k if cu_seqlens_k.is_contiguous() else cu_seqlens_k.contiguous())
 
 
 def _slopes_for(alibi_slopes: Optional[torch.Tensor], hq: int, idx: int):
@@ -473,9 +486,7 @@ def _slopes_for(alibi_slopes: Optional[torch.Tensor], hq: int, idx: int):
     return _dense(alibi_slopes)
 
 
-def _scale_for(scale: Optional[float], d: int) -> float:
-    if scale is not None:
-        return float(scale)
+def _inv_sqrt(d: int) -> float:
     inv = _INV_SQRT.get(d)
     if inv is None:
         inv = _INV_SQRT[d] = 1.0 / math.sqrt(d) if d > 0 else 0.0
@@ -494,13 +505,15 @@ def _output(name, t, shape, dtype, idx: int) -> torch.Tensor:
     return t
 
 
-def _scratch(t: Optional[torch.Tensor], size, idx: int):
-    """The workspace (made here, of ``size()`` bytes, when the caller gives none) and its bytes."""
-    if t is None:
-        t = torch.empty(size(), dtype=torch.uint8, device=f"cuda:{idx}")
-    elif t.get_device() != idx or not t.is_contiguous():
+def _scratch(t: torch.Tensor, idx: int) -> int:
+    """A workspace's bytes."""
+    if t.get_device() != idx or not t.is_contiguous():
         raise MeaError(_lib.MEA_ERR_WORKSPACE, f"workspace must be contiguous on cuda:{idx}")
-    return t, t.numel() * t.element_size()
+    return t.numel() * t.element_size()
+
+
+def _new_scratch(size: int, idx: int) -> torch.Tensor:
+    return torch.empty(size, dtype=torch.uint8, device=f"cuda:{idx}")
 
 
 def _check_weights(name: str, t: torch.Tensor, n: int, hkv: int, max_k: int, idx: int) -> int:
@@ -529,10 +542,6 @@ def _launch(idx: int, name: str, *args) -> None:
         raise MeaError(rc, name)
 
 
-def _addr(t: Optional[torch.Tensor]) -> int:
-    return 0 if t is None else t.data_ptr()
-
-
 def block_key_bounds(k_cache: torch.Tensor, block_table: torch.Tensor,
                      cu_seqlens_k: torch.Tensor, max_seqlen_k: int,
                      first_key: Optional[torch.Tensor] = None,
@@ -545,15 +554,16 @@ def block_key_bounds(k_cache: torch.Tensor, block_table: torch.Tensor,
     idx, (nb, bs, hkv, d), code, table, cu = _check_paged(k_cache, None, block_table,
                                                           cu_seqlens_k)
     n, max_blocks = table.shape
-    first = None
+    first_at = 0
     if first_key is not None:
         first = _check_prefix("first_key", first_key, n, idx)
+        first_at = first.data_ptr()
     if bounds is None:
         bounds = torch.zeros((nb, hkv, 2, d), dtype=k_cache.dtype, device=k_cache.device)
     else:
         _output("bounds", bounds, (nb, hkv, 2, d), k_cache.dtype, idx)
     _launch(idx, "mea_block_key_bounds", k_cache.data_ptr(), table.data_ptr(), cu.data_ptr(),
-            _addr(first), bounds.data_ptr(), n, nb, bs, max_blocks, int(max_seqlen_k), hkv, d, code)
+            first_at, bounds.data_ptr(), n, nb, bs, max_blocks, int(max_seqlen_k), hkv, d, code)
     return bounds
 
 
@@ -603,9 +613,9 @@ def decode_paged_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
                           selected: torch.Tensor, alibi_slopes: Optional[torch.Tensor] = None,
                           scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
                           out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None):
-    """:func:`decode_paged` over the blocks in ``selected`` (:func:`select_blocks`) only. Entries may
-    be in any order; one below 0 or past the request's blocks names no keys, a block listed twice
-    counts twice. Returns ``(out [n_seqs, Hq, D], lse [Hq, n_seqs])``."""
+    """:func:`decode_paged` over the blocks in ``selected`` (:func:`select_blocks`) only. Entries
+    may be in any order; one below 0 or past the request's blocks names no keys, a block listed
+    twice counts twice. Returns ``(out [n_seqs, Hq, D], lse [Hq, n_seqs])``."""
     idx, (nb, bs, hkv, d), code, table, cu = _check_paged(k_cache, v_cache, block_table,
                                                           cu_seqlens_k, q)
     q = _dense(q)
@@ -616,15 +626,18 @@ def decode_paged_selected(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch
     _same_gpu("selected", selected, idx)
     selected = _dense(selected)
     n_select = selected.size(2)
-    ws, ws_bytes = _scratch(workspace, lambda: decode_selected_workspace_size(
+    ws = workspace if workspace is not None else _new_scratch(decode_selected_workspace_size(
         n, n_select, bs, hq, hkv, d), idx)
+    ws_bytes = _scratch(ws, idx)
     out = _output("out", out, (n, hq, d), q.dtype, idx)
     lse = _output("lse", lse, (hq, n), torch.float32, idx)
-    slopes = _slopes_for(alibi_slopes, hq, idx)
+    slopes = None if alibi_slopes is None else _slopes_for(alibi_slopes, hq, idx)
+    slopes_at = 0 if slopes is None else slopes.data_ptr()
+    scale = _inv_sqrt(d) if scale is None else float(scale)
     _launch(idx, "mea_decode_selected", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             table.data_ptr(), cu.data_ptr(), selected.data_ptr(), out.data_ptr(), lse.data_ptr(),
-            n, nb, bs, table.size(1), n_select, hq, hkv, d, _scale_for(scale, d), _addr(slopes),
-            code, ws.data_ptr(), ws_bytes)
+            n, nb, bs, table.size(1), n_select, hq, hkv, d, scale, slopes_at, code, ws.data_ptr(),
+            ws_bytes)
     return out, lse
 
 
@@ -653,18 +666,23 @@ def decode_paged_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
         raise MeaError(_lib.MEA_ERR_SHAPE, "block_table must have a row per request")
     max_k = int(max_seqlen_k)
     width = _check_weights("weights", weights, n, hkv, max_k, idx)
+    prev_at = 0
     if prev_weights is not None:
-        _output("prev_weights", prev_weights, weights.shape, torch.float32, idx)
+        prev_at = _output("prev_weights", prev_weights, weights.shape, torch.float32,
+                          idx).data_ptr()
     total = int(total_k_bound) if total_k_bound is not None else nb * bs
-    ws, ws_bytes = _scratch(workspace, lambda: decode_weights_workspace_size(
+    ws = workspace if workspace is not None else _new_scratch(decode_weights_workspace_size(
         n, total, hq, hkv, d, split_keys), idx)
+    ws_bytes = _scratch(ws, idx)
     out = _output("out", out, (n, hq, d), q.dtype, idx)
     lse = _output("lse", lse, (hq, n), torch.float32, idx)
-    slopes = _slopes_for(alibi_slopes, hq, idx)
+    slopes = None if alibi_slopes is None else _slopes_for(alibi_slopes, hq, idx)
+    slopes_at = 0 if slopes is None else slopes.data_ptr()
+    scale = _inv_sqrt(d) if scale is None else float(scale)
     _launch(idx, "mea_decode_weights", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             table.data_ptr(), cu.data_ptr(), out.data_ptr(), lse.data_ptr(), weights.data_ptr(),
-            _addr(prev_weights), width, n, nb, bs, table.size(1), total, max_k, hq, hkv, d,
-            _scale_for(scale, d), _addr(slopes), code, ws.data_ptr(), ws_bytes, int(split_keys))
+            prev_at, width, n, nb, bs, table.size(1), total, max_k, hq, hkv, d, scale, slopes_at,
+            code, ws.data_ptr(), ws_bytes, int(split_keys))
     return out, lse, weights
 
 
@@ -680,10 +698,10 @@ def attention_packed_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor
                              weights: Optional[torch.Tensor] = None,
                              workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The attention weight that a packed batch's queries put on its keys, for
-    :func:`attention_packed` called with the same arguments (``lse`` is its result): ``weights`` fp32
-    ``[n_seqs, Hkv, >= max_seqlen_k]``, summed over the heads of a KV group and over the queries
-    (``last_queries`` > 0: each segment's last ones only). Entries past a segment's keys are left as
-    they were (zeros when ``weights`` is made here)."""
+    :func:`attention_packed` called with the same arguments (``lse`` is its result): ``weights``
+    fp32 ``[n_seqs, Hkv, >= max_seqlen_k]``, summed over the heads of a KV group and over the
+    queries (``last_queries`` > 0: each segment's last ones only). Entries past a segment's keys are
+    left as they were (zeros when ``weights`` is made here)."""
     idx = _gpu_index(q)
     if q.dim() != 3 or k.dim() != 3 or k.size(2) != q.size(2):
         raise MeaError(_lib.MEA_ERR_SHAPE, "q [T_q, Hq, D], k [T_k, Hkv, D]")
@@ -702,13 +720,17 @@ def attention_packed_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor
     if weights is None:
         weights = torch.zeros((n, hkv, max_k), dtype=torch.float32, device=q.device)
     width = _check_weights("weights", weights, n, hkv, max_k, idx)
-    ws, ws_bytes = _scratch(workspace, lambda: attention_weights_workspace_size(d), idx)
-    slopes = _slopes_for(alibi_slopes, hq, idx)
+    ws = workspace if workspace is not None else _new_scratch(
+        attention_weights_workspace_size(d), idx)
+    ws_bytes = _scratch(ws, idx)
+    slopes = None if alibi_slopes is None else _slopes_for(alibi_slopes, hq, idx)
+    slopes_at = 0 if slopes is None else slopes.data_ptr()
+    scale = _inv_sqrt(d) if scale is None else float(scale)
     _launch(idx, "mea_attention_weights", q.data_ptr(), k.data_ptr(), lse.data_ptr(),
             cu_q.data_ptr(), cu_k.data_ptr(), weights.data_ptr(), width, n, tq, tk,
-            int(max_seqlen_q), max_k, hq, hkv, d, _scale_for(scale, d),
-            _lib.MEA_MASK_CAUSAL if causal else _lib.MEA_MASK_NONE, _addr(slopes),
-            int(last_queries), _dtype_code(q.dtype), ws.data_ptr(), ws_bytes)
+            int(max_seqlen_q), max_k, hq, hkv, d, scale, _lib.MEA_MASK_CAUSAL if causal else
+            _lib.MEA_MASK_NONE, slopes_at, int(last_queries), _dtype_code(q.dtype), ws.data_ptr(),
+            ws_bytes)
     return weights
 
 
@@ -749,8 +771,8 @@ def evict_paged(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch
     _launch(idx, "mea_evict_paged", k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(),
             cu.data_ptr(), weights.data_ptr(), width, ko.data_ptr(), vo.data_ptr(),
             out_table.data_ptr(), kept.data_ptr(), ow.data_ptr(), ocu.data_ptr(), n, nb,
-            out_shape[0], bs, max_blocks, out_table.size(1), max_k, hkv, d, n_keep,
-            int(n_recent), code)
+            out_shape[0], bs, max_blocks, out_table.size(1), max_k, hkv, d, n_keep, int(n_recent),
+            code)
     return kept, ow, ocu
 
 
@@ -798,17 +820,20 @@ def decode_tree_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         raise MeaError(_lib.MEA_ERR_SHAPE, f"tree_mask must be int32 [{tq}, words]")
     _same_gpu("tree_mask", tree_mask, idx)
     mask = _dense(tree_mask)
-    ws, ws_bytes = _scratch(workspace, lambda: decode_tree_workspace_size(hq, hkv, d), idx)
+    ws = workspace if workspace is not None else _new_scratch(
+        decode_tree_workspace_size(hq, hkv, d), idx)
+    ws_bytes = _scratch(ws, idx)
     out = _output("out", out, (tq, hq, d), q.dtype, idx)
     lse = _output("lse", lse, (hq, tq), torch.float32, idx)
-    slopes = _slopes_for(alibi_slopes, hq, idx)
+    slopes = None if alibi_slopes is None else _slopes_for(alibi_slopes, hq, idx)
+    slopes_at = 0 if slopes is None else slopes.data_ptr()
+    scale = _inv_sqrt(d) if scale is None else float(scale)
     if tq == 0:
         return out, lse
     _launch(idx, "mea_decode_tree", q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
             table.data_ptr(), cu_q.data_ptr(), cu_k.data_ptr(), mask.data_ptr(), out.data_ptr(),
             lse.data_ptr(), n, tq, int(max_seqlen_q), int(max_seqlen_k), mask.size(1), nb, bs,
-            table.size(1), hq, hkv, d, _scale_for(scale, d), _addr(slopes), code, ws.data_ptr(),
-            ws_bytes)
+            table.size(1), hq, hkv, d, scale, slopes_at, code, ws.data_ptr(), ws_bytes)
     return out, lse
 
 
