@@ -426,6 +426,7 @@ int mea_evict_paged(const void* k_cache, const void* v_cache, const int32_t* blo
   // Rank keys in shared memory for up to 48 Ki keys; longer rows are read again in every pass.
   constexpr int max_keys = 48 * 1024;
   p.smem_keys = max_seqlen_k < max_keys ? max_seqlen_k : max_keys;
+  p.longest_first = pairs > di.sms && n_seqs > 1 && n_seqs <= mea::kEvictThreads;
   constexpr auto sel = mea::mea_evict_select_kernel;
   if (smem_attr_once<sel>(max_keys * 4) != cudaSuccess) return MEA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -318,6 +318,43 @@ def test_evict(lens, hkv, d, dtype, bs, keep, recent, same):
     assert torch.equal(ko[~written].nan_to_num(7.0), before[~written].nan_to_num(7.0))
 
 
+@pytest.mark.parametrize("kind", ["spread", "close", "equal", "ties at the cut"])
+@pytest.mark.parametrize("lens,hkv,keep,recent", [
+    ([3001], 2, 700, 40),
+    ([int(9 + 61 * i % 1300) for i in range(40)], 4, 150, 9),   # more (request, head)s than SMs
+    ([60001], 1, 2000, 7),                                      # more keys than shared memory holds
+])
+def test_evict_selects_whatever_the_weights_range(lens, hkv, keep, recent, kind):
+    n, bs = len(lens), 32
+    c = ref.Cache(lens, hkv, hkv, 8, BF, bs, 76)
+    w = randn((n, hkv, c.max), 77, torch.float32)
+    if kind == "spread":
+        w = torch.exp(12 * w)  # some 100 binades
+    elif kind == "close":
+        w = 1 + w.abs() * 2.0 ** -18
+    elif kind == "equal":
+        w = torch.full_like(w, 0.125)
+    else:
+        w = torch.where(w > 0.5, w, torch.full_like(w, 0.25))
+    per = -(-keep // bs)
+    ids = torch.arange(n * per, dtype=torch.int32).view(n, per)
+    kc, vc, table, cu = c.gpu()
+    ko = torch.zeros((n * per, bs, hkv, 8), dtype=BF, device="cuda")
+    kept, ow, _ = mea.evict_paged(kc, vc, table, cu, c.max, w.cuda(), keep, recent, ids.cuda(),
+                                  out_k_cache=ko, out_v_cache=torch.zeros_like(ko))
+    kept, ow, ko = kept.cpu(), ow.cpu(), ko.cpu()
+    for b, length in enumerate(lens):
+        m = max(0, length - recent)
+        for g in range(hkv):
+            order = torch.sort(w[b, g, :m], descending=True, stable=True).indices.tolist()
+            want = sorted(order[:max(0, min(length, keep) - min(recent, length))])
+            want += list(range(m, length))
+            assert kept[b, g].tolist() == want + [-1] * (keep - len(want))
+            assert torch.equal(ow[b, g, :len(want)], w[b, g, want])
+            t = torch.arange(len(want))
+            assert torch.equal(ko[ids[b, t // bs].long(), t % bs, g], c.k[b][want, g])
+
+
 def test_evict_ranks_nan_and_infinities():
     c = ref.Cache([10], 1, 1, 16, BF, 16, 75)
     kc, vc, table, cu = c.gpu()
