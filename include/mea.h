@@ -234,7 +234,7 @@ int mea_backward(const void* q, const void* k, const void* v, const void* out, c
  *   cu_seqlens_k      DEVICE int32 [n_seqs + 1], prefix sums of the requests' key counts L_b.
  *   block_size        16, 32, or a multiple of 64.
  *   total_k           an upper bound on cu_seqlens_k[n_seqs] (for example num_blocks *
- *                     block_size); it sizes the workspace exactly as in mea_decode_splitkv:
+ *                     block_size where no two requests share a block); it sizes the workspace exactly as in mea_decode_splitkv:
  *                     mea_decode_workspace_size(n_seqs, total_k, ...).
  *   max_seqlen_k      an upper bound on every L_b, at most max_blocks * block_size.
  * Slots of a block past the end of its sequence may hold any bits (they are never used).

@@ -309,7 +309,9 @@ def decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  total_k_bound: Optional[int] = None, out: Optional[torch.Tensor] = None,
                  lse: Optional[torch.Tensor] = None):
     """Split-KV decode over a paged cache ``[num_blocks, block_size, Hkv, D]`` with an int32
-    ``block_table [n_seqs, max_blocks]``. Returns ``(out [n_seqs, Hq, D], lse [Hq, n_seqs])``."""
+    ``block_table [n_seqs, max_blocks]``. Where requests share blocks, ``total_k_bound`` has to be
+    given: at least the requests' key counts together (None: the cache's slots). Returns
+    ``(out [n_seqs, Hq, D], lse [Hq, n_seqs])``."""
     for t in (q, k_cache, v_cache, block_table, cu_seqlens_k):
         if not t.is_cuda:
             raise MeaError(_lib.MEA_ERR_DEVICE, "tensors must live on the GPU")
@@ -657,7 +659,9 @@ def decode_paged_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     """:func:`decode_paged` that also writes each key's attention weight, summed over the heads of
     its KV group and added to ``prev_weights`` (None: zeros; ``weights`` itself: accumulate in
     place), to ``weights`` fp32 ``[n_seqs, Hkv, >= max_seqlen_k]``; entries past a request's keys
-    are left as they were. Returns ``(out [n_seqs, Hq, D], lse [Hq, n_seqs], weights)``."""
+    are left as they were. ``total_k_bound``: an upper bound on the requests' key counts together,
+    for the workspace (None: ``n_seqs * max_seqlen_k``, since requests may share blocks). Returns
+    ``(out [n_seqs, Hq, D], lse [Hq, n_seqs], weights)``."""
     idx, (nb, bs, hkv, d), code, table, cu = _check_paged(k_cache, v_cache, block_table,
                                                           cu_seqlens_k, q)
     q = _dense(q)
@@ -670,7 +674,7 @@ def decode_paged_weights(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     if prev_weights is not None:
         prev_at = _output("prev_weights", prev_weights, weights.shape, torch.float32,
                           idx).data_ptr()
-    total = int(total_k_bound) if total_k_bound is not None else nb * bs
+    total = int(total_k_bound) if total_k_bound is not None else min(n * max_k, 0x7fffffff)
     ws = workspace if workspace is not None else _new_scratch(decode_weights_workspace_size(
         n, total, hq, hkv, d, split_keys), idx)
     ws_bytes = _scratch(ws, idx)

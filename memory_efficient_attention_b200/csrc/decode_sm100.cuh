@@ -681,13 +681,14 @@ __device__ __forceinline__ void dec_merge(const DecParams& p, int b, int g) {
   __shared__ int s_start;
   __shared__ float s_m[64], s_z[64];
   const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
-  const int n = (L + p.chunk - 1) / p.chunk;
   if (threadIdx.x < 32) {
     const int st = dec_chunk_start(p.cu_k, b, p.chunk);
     if (threadIdx.x == 0) s_start = st;
   }
   __syncthreads();
   const int c0 = s_start;
+  // (never past the workspace, should the key counts exceed the bound they were sized by)
+  const int n = min((L + p.chunk - 1) / p.chunk, p.n_slots - c0);
   using OutT = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   OutT* out = reinterpret_cast<OutT*>(p.out);
   for (int rb = 0; rb < p.R; rb += 64) {  // heads of the group, 64 at a time

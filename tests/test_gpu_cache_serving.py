@@ -159,6 +159,42 @@ def test_a_step_replays_in_a_cuda_graph_and_on_another_stream():
     assert mea.device_error() == 0
 
 
+@pytest.mark.parametrize("split", [0, 64])
+def test_requests_that_share_their_first_blocks(split):
+    """Three requests with one prefix: together they have more keys than the cache has slots."""
+    length, hq, hkv, d, bs, dtype = 1200, 8, 2, 64, 16, BF
+    c = ref.Cache([length], hq, hkv, d, dtype, bs, 91, extra=8)
+    c.lens = [1200, 1200, 960]
+    c.k, c.v = [c.k[0][:n] for n in c.lens], [c.v[0][:n] for n in c.lens]
+    c.table, c.cu = c.table.expand(3, -1).contiguous(), cu_seqlens(c.lens)
+    assert sum(c.lens) > c.num_blocks * bs
+    q = randn((3, hq, d), 92, dtype)
+    kc, vc, table, cu = c.gpu()
+    w = torch.zeros((3, hkv, length), device="cuda")
+    out, lse, _ = mea.decode_paged_weights(q.cuda(), kc, vc, table, cu, length, w, scale=0.125,
+                                           split_keys=split)
+    o, m, z, want = ref.decode(c, q, 0.125)
+    ref.check_out(out.cpu(), lse.cpu(), o, m, z, dtype)
+    for b, n in enumerate(c.lens):
+        x = torch.stack(want[b])
+        assert bool(((w.cpu()[b, :, :n].double() - x).abs() <=
+                     ref.F32 * x + 2.0 ** -23 * x * (hq // hkv) + 1e-30).all())
+        assert not bool(w[b, :, n:].any())
+    bounds = mea.block_key_bounds(kc, table, cu, length)
+    full, used = ref.block_bounds(c)
+    assert torch.equal(bounds.cpu()[used], full[used])
+    sel = mea.select_blocks(q.cuda(), bounds, table, cu, length, bs, 9)
+    assert sel.cpu().tolist() == ref.choose(c, q, full, 9, 1, 1)
+    # Tokens drafted for all three: their keys lie in the shared blocks here.
+    nq = [5, 3, 16]
+    tq = randn((sum(nq), hq, d), 93, dtype)
+    chain = [list(range(-1, n - 1)) for n in nq]
+    got, gl = mea.decode_tree_paged(tq.cuda(), kc, vc, table, cu_seqlens(nq).cuda(), cu, 16, length,
+                                    mea.tree_mask(chain).cuda(), scale=0.125)
+    o, m, z = ref.tree(c, tq, nq, [torch.ones(n, n, dtype=torch.bool).tril() for n in nq], 0.125)
+    ref.check_out(got.cpu(), gl.cpu(), o, m, z, dtype)
+
+
 def test_two_streams_at_once():
     """Two steps in flight together, each with its own buffers and workspace."""
     a, b = _state(), _state()
