@@ -195,6 +195,47 @@ def test_requests_that_share_their_first_blocks(split):
     ref.check_out(got.cpu(), gl.cpu(), o, m, z, dtype)
 
 
+def test_rows_behind_the_last_request_stay():
+    """Buffers longer than the batch, and bounds on the lengths that are too large, as a captured step
+    has them: what lies behind the last request is neither read nor written."""
+    lens, nq, hq, hkv, d, bs = [300, 0, 77], [5, 0, 33], 8, 2, 128, 16
+    c = ref.Cache(lens, hq, hkv, d, BF, bs, 94)
+    kc, vc, table, cu = c.gpu()
+    table = torch.cat((table, torch.full((3, 100), 1 << 30, dtype=torch.int32, device="cuda")), 1)
+    rows, tq = sum(nq), sum(nq) + 40
+    q = randn((tq, hq, d), 95, BF)
+    q[rows:] = math.nan
+    chain = [list(range(-1, n - 1)) for n in nq]
+    mask = torch.full((tq, 4), -1, dtype=torch.int32)
+    mask[:rows, :2] = mea.tree_mask(chain)
+    before = randn((tq, hq, d), 96, BF)
+    lse0 = randn((hq, tq), 97, torch.float32)
+    out, lse = before.cuda(), lse0.cuda()
+    mea.decode_tree_paged(q.cuda(), kc, vc, table, cu_seqlens(nq).cuda(), cu, 78, 1800, mask.cuda(),
+                          scale=0.09, out=out, lse=lse)
+    o, m, z = ref.tree(c, q[:rows], nq, [torch.ones(n, n, dtype=torch.bool).tril() for n in nq],
+                       0.09)
+    ref.check_out(out.cpu()[:rows], lse.cpu()[:, :rows], o, m, z, BF)
+    assert torch.equal(out.cpu()[rows:], before[rows:])
+    assert torch.equal(lse.cpu()[:, rows:], lse0[:, rows:])
+    # A packed prompt with rows of padding.
+    pq, pk, pv = make_qkv(lens, lens, hq, hkv, d, BF, 98)
+    cuq = cu_seqlens(lens).cuda()
+    _, pl = mea.attention_packed(pq.cuda(), pk.cuda(), pv.cuda(), cuq, cuq, 300, causal=True)
+    want = mea.attention_packed_weights(pq.cuda(), pk.cuda(), pl, cuq, cuq, 300, 300, causal=True)
+    pad = torch.full((50, hq, d), math.nan, dtype=BF)
+    w = torch.full((3, hkv, 400), 7.0, device="cuda")
+    got = mea.attention_packed_weights(
+        torch.cat((pq, pad)).cuda(), torch.cat((pk, pad[:, :hkv])).cuda(),
+        torch.cat((pl, torch.full((hq, 50), math.nan, device="cuda")), 1).contiguous(), cuq, cuq,
+        400, 400, causal=True, weights=w)
+    for b, n in enumerate(lens):
+        # (other bounds may cut the sums elsewhere: fp32 rounding)
+        assert bool(((got[b, :, :n] - want[b, :, :n]).abs() <= ref.F32 * want[b, :, :n]).all())
+        assert bool((got[b, :, n:] == 7.0).all())
+    assert mea.device_error() == 0
+
+
 def test_two_streams_at_once():
     """Two steps in flight together, each with its own buffers and workspace."""
     a, b = _state(), _state()
