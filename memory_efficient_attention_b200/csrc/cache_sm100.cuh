@@ -783,7 +783,7 @@ __global__ void __launch_bounds__(256) mea_evict_copy_kernel(const EvictParams p
     const int i = tile * kEvictRows + threadIdx.x;
     long long src = -1, dst = -1;
     if (threadIdx.x < n) {
-      const int t = __ldg(p.kept + static_cast<size_t>(pair) * p.n_keep + i);
+      const int t = ld_after_wait(p.kept + static_cast<size_t>(pair) * p.n_keep + i);
       const int js = t / p.block_size, jd = i / p.block_size;
       if (js < p.max_blocks && jd < p.max_out_blocks) {
         const int is = __ldg(p.block_table + static_cast<size_t>(b) * p.max_blocks + js);

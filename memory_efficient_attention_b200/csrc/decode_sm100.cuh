@@ -175,6 +175,15 @@ struct DecRange {
   }
 };
 
+// Reads a word of the inputs. The split kernel of DEC_SELECTED is launched as a dependent of
+// whatever ran before it (a block choice, or the caller's own kernel), which may have written any
+// of them.
+template <int MODE, class T>
+__device__ __forceinline__ T dec_ld(const T* ptr) {
+  if constexpr (MODE == DEC_SELECTED) return ld_after_wait(ptr);
+  return __ldg(ptr);
+}
+
 // Warp-cooperative: keys of the (request b, KV head g) list from key0 on, up to key1 and the end of
 // the last entry that names a block (entries after that load and add nothing).
 __device__ __forceinline__ int dec_selected_keys(const DecParams& p, int b, int g, int key0,
@@ -185,7 +194,7 @@ __device__ __forceinline__ int dec_selected_keys(const DecParams& p, int b, int 
   const int32_t* list = p.selected + (static_cast<size_t>(b) * (p.hq / p.R) + g) * p.n_select;
   int live = 0;
   for (int i = e0 + lane; i < e1; i += 32)
-    if (__ldg(list + i) >= 0) live = i + 1;
+    if (ld_after_wait(list + i) >= 0) live = i + 1;
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1)
     live = max(live, __shfl_xor_sync(0xffffffffu, live, off));
@@ -258,8 +267,8 @@ __global__ void __launch_bounds__(160, 1)
         dec_find_chunk(p.cu_k, p.n_seqs, p.chunk, cid, b, c);
         if (b < 0) break;  // flat chunk ids only grow along this CTA's sequence
       }
-      const int k0 = __ldg(p.cu_k + b);
-      const int L = __ldg(p.cu_k + b + 1) - k0;
+      const int k0 = dec_ld<MODE>(p.cu_k + b);
+      const int L = dec_ld<MODE>(p.cu_k + b + 1) - k0;
       const int key0 = MODE == DEC_SELECTED ? t0 * C::BK : c * p.chunk;
       const int g = (hb * p.RB) / p.R;
       int nk;
@@ -293,10 +302,10 @@ __global__ void __launch_bounds__(160, 1)
         auto block_id = [&](int t) {
           int j = (key0 + t * C::BK + my_i * bs) / bs;
           if constexpr (MODE == DEC_SELECTED) {
-            j = (issuer && t < n_tiles && j < p.n_select) ? __ldg(list + j) : -1;
-            return (j >= 0 && j < nblk) ? __ldg(row + j) : p.num_blocks;
+            j = (issuer && t < n_tiles && j < p.n_select) ? dec_ld<MODE>(list + j) : -1;
+            return (j >= 0 && j < nblk) ? dec_ld<MODE>(row + j) : p.num_blocks;
           }
-          return (issuer && t < n_tiles && j < nblk) ? __ldg(row + j) : p.num_blocks;
+          return (issuer && t < n_tiles && j < nblk) ? dec_ld<MODE>(row + j) : p.num_blocks;
         };
         // Block ids of tiles t .. t+3: each read is in flight for three tiles before its TMA
         // needs it (a block-table line that misses in L2 waits on HBM under a full load).
@@ -384,7 +393,7 @@ __global__ void __launch_bounds__(160, 1)
         dec_find_chunk(p.cu_k, p.n_seqs, p.chunk, cid, b, c);
         if (b < 0) break;
       }
-      const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
+      const int L = dec_ld<MODE>(p.cu_k + b + 1) - dec_ld<MODE>(p.cu_k + b);
       const int key0 = MODE == DEC_SELECTED ? t0 * C::BK : c * p.chunk;
       int nk;
       if constexpr (MODE == DEC_SELECTED)
@@ -406,16 +415,16 @@ __global__ void __launch_bounds__(160, 1)
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const bool c0 = kk * 8 + t4 < dw, c1 = kk * 8 + 4 + t4 < dw;
-          qa[kk][0] = (v_lo && c0) ? __ldg(q32 + rlo + kk * 8 + t4) : 0u;
-          qa[kk][1] = (v_hi && c0) ? __ldg(q32 + rhi + kk * 8 + t4) : 0u;
-          qa[kk][2] = (v_lo && c1) ? __ldg(q32 + rlo + kk * 8 + 4 + t4) : 0u;
-          qa[kk][3] = (v_hi && c1) ? __ldg(q32 + rhi + kk * 8 + 4 + t4) : 0u;
+          qa[kk][0] = (v_lo && c0) ? dec_ld<MODE>(q32 + rlo + kk * 8 + t4) : 0u;
+          qa[kk][1] = (v_hi && c0) ? dec_ld<MODE>(q32 + rhi + kk * 8 + t4) : 0u;
+          qa[kk][2] = (v_lo && c1) ? dec_ld<MODE>(q32 + rlo + kk * 8 + 4 + t4) : 0u;
+          qa[kk][3] = (v_hi && c1) ? dec_ld<MODE>(q32 + rhi + kk * 8 + 4 + t4) : 0u;
         }
       }
       float sl_lo = 0.f, sl_hi = 0.f;
       if constexpr (ALIBI) {
-        sl_lo = v_lo ? __ldg(p.slopes + h_lo) * LOG2E : 0.f;
-        sl_hi = v_hi ? __ldg(p.slopes + h_hi) * LOG2E : 0.f;
+        sl_lo = v_lo ? dec_ld<MODE>(p.slopes + h_lo) * LOG2E : 0.f;
+        sl_hi = v_hi ? dec_ld<MODE>(p.slopes + h_hi) * LOG2E : 0.f;
       }
       float m_lo = -INFINITY, m_hi = -INFINITY, l_lo = 0.f, l_hi = 0.f;
       float o[D / 8][4];
@@ -426,9 +435,9 @@ __global__ void __launch_bounds__(160, 1)
       auto entry = [&](int t) {
         const int j = (key0 + t * C::BK + warp * 16) / p.block_size;
         return (t < n_tiles && j < p.n_select)
-                   ? __ldg(p.selected +
-                           (static_cast<size_t>(b) * (p.hq / p.R) + (hb * p.RB) / p.R) *
-                               p.n_select + j)
+                   ? dec_ld<MODE>(p.selected +
+                                  (static_cast<size_t>(b) * (p.hq / p.R) + (hb * p.RB) / p.R) *
+                                      p.n_select + j)
                    : -1;
       };
       int e_next = MODE == DEC_SELECTED ? entry(0) : 0;

@@ -157,7 +157,9 @@ cudaError_t smem_attr_once(uint32_t smem) {
 inline void clear_stale_launch_error() { (void)cudaGetLastError(); }
 
 // Launches `kern` as the dependent of the stream's previous kernel: it may start before that one
-// has ended and calls pdl_wait before it touches anything that one reads or writes.
+// has ended and calls pdl_wait before it touches anything that one reads or writes. What that one
+// writes is read by ld_after_wait or a plain load, never by __ldg, which stays for buffers that were
+// complete before that one was launched.
 template <class... Params, class... Args>
 cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, dim3 block, size_t smem,
                              cudaStream_t stream, Args&&... args) {

@@ -234,6 +234,15 @@ __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
+// A load of data that the kernel before a dependent launch may have written: an ordinary one, which
+// the wait's memory clobber keeps behind it. __ldg is for what nothing writes while the kernel lives
+// (its path need not see such writes, and the compiler may move it ahead of the wait), and a
+// dependent launch lives from before the end of the kernel that it depends on.
+template <class T>
+__device__ __forceinline__ T ld_after_wait(const T* p) {
+  return *p;
+}
+
 // L1 prefetch of the line holding addr (a hint).
 __device__ __forceinline__ void prefetch_l1(const void* addr) {
   asm volatile("prefetch.global.L1 [%0];" ::"l"(addr));
