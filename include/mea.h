@@ -233,9 +233,12 @@ int mea_backward(const void* q, const void* k, const void* v, const void* out, c
  *                     are not read. An id outside [0, num_blocks) reads as zeros (never faults).
  *   cu_seqlens_k      DEVICE int32 [n_seqs + 1], prefix sums of the requests' key counts L_b.
  *   block_size        16, 32, or a multiple of 64.
- *   total_k           an upper bound on cu_seqlens_k[n_seqs] (for example num_blocks *
- *                     block_size where no two requests share a block); it sizes the workspace exactly as in mea_decode_splitkv:
- *                     mea_decode_workspace_size(n_seqs, total_k, ...).
+ *   total_k           an upper bound on cu_seqlens_k[n_seqs], for example num_blocks * block_size;
+ *                     it sizes the workspace exactly as in mea_decode_splitkv:
+ *                     mea_decode_workspace_size(n_seqs, total_k, ...). (Requests that share blocks
+ *                     may hold more keys than that, as long as total_k >= 1: the chunks they are
+ *                     split into are then longer than split_keys, and the result is the same
+ *                     softmax.)
  *   max_seqlen_k      an upper bound on every L_b, at most max_blocks * block_size.
  * Slots of a block past the end of its sequence may hold any bits (they are never used).
  */

@@ -309,8 +309,9 @@ def decode_paged(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                  total_k_bound: Optional[int] = None, out: Optional[torch.Tensor] = None,
                  lse: Optional[torch.Tensor] = None):
     """Split-KV decode over a paged cache ``[num_blocks, block_size, Hkv, D]`` with an int32
-    ``block_table [n_seqs, max_blocks]``. Where requests share blocks, ``total_k_bound`` has to be
-    given: at least the requests' key counts together (None: the cache's slots). Returns
+    ``block_table [n_seqs, max_blocks]``. ``total_k_bound``: about the requests' key counts
+    together, which size the workspace (None: the cache's slots). Requests that share blocks may
+    hold more: they are then split into longer chunks. Returns
     ``(out [n_seqs, Hq, D], lse [Hq, n_seqs])``."""
     for t in (q, k_cache, v_cache, block_table, cu_seqlens_k):
         if not t.is_cuda:

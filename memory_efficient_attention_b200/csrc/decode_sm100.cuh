@@ -52,6 +52,7 @@ struct DecParams {
   int n_hb;           // hq / RB
   int chunk;          // keys per chunk, a multiple of 64
   int n_slots;        // upper bound on the number of chunks
+  int may_exceed;     // (paged) the requests may hold more keys than n_slots was sized by
   long long n_items;  // n_slots * n_hb
   float c1;           // scale * log2(e)
   unsigned long long timeout_ns;
@@ -105,6 +106,19 @@ struct DecCfg {
 __device__ __forceinline__ int dec_nchunks(const int32_t* cu, int i, int chunk) {
   const int L = __ldg(cu + i + 1) - __ldg(cu + i);
   return (L + chunk - 1) / chunk;
+}
+
+// Keys per chunk. A paged decode's slots are sized by a bound on the requests' keys together (the
+// cache's slots, where the caller gives none), which requests that share blocks can exceed. Then the
+// chunks are as many times longer as the keys K exceed it, and the slots hold all of them:
+//     sum_b ceil(L_b / chunk) <= K / chunk + n_seqs <= n_slots.
+// (The loads of K take at most 2 us of a call of 803: 64 requests of up to 32768 keys, 16 slots.)
+__device__ __forceinline__ int dec_chunk(const DecParams& p) {
+  if (!p.may_exceed) return p.chunk;
+  const long long room = static_cast<long long>(p.n_slots - p.n_seqs) * p.chunk;
+  const long long keys = static_cast<long long>(__ldg(p.cu_k + p.n_seqs)) - __ldg(p.cu_k);
+  if (keys <= room || room <= 0) return p.chunk;
+  return static_cast<int>(min(div_nn(keys + room - 1, room) * p.chunk, 1ll << 30));
 }
 
 // Warp-cooperative: maps a flat chunk id to (request b, chunk c of b); b = -1 past the end.
@@ -246,6 +260,7 @@ __global__ void __launch_bounds__(160, 1)
     if constexpr (MODE == DEC_SELECTED) pdl_wait();  // the block choice may be still running
   }
 
+  const int chunk = PAGED && MODE == DEC_ALL ? dec_chunk(p) : p.chunk;
   if (warp == 4) {
     // ------------------------------------------------------------------ TMA producer
     uint32_t cnt = 0;
@@ -264,18 +279,18 @@ __global__ void __launch_bounds__(160, 1)
       const int hb = static_cast<int>(item - static_cast<long long>(cid) * p.n_hb);
       int b = cid, c = 0;
       if constexpr (MODE != DEC_SELECTED) {
-        dec_find_chunk(p.cu_k, p.n_seqs, p.chunk, cid, b, c);
+        dec_find_chunk(p.cu_k, p.n_seqs, chunk, cid, b, c);
         if (b < 0) break;  // flat chunk ids only grow along this CTA's sequence
       }
       const int k0 = dec_ld<MODE>(p.cu_k + b);
       const int L = dec_ld<MODE>(p.cu_k + b + 1) - k0;
-      const int key0 = MODE == DEC_SELECTED ? t0 * C::BK : c * p.chunk;
+      const int key0 = MODE == DEC_SELECTED ? t0 * C::BK : c * chunk;
       const int g = (hb * p.RB) / p.R;
       int nk;
       if constexpr (MODE == DEC_SELECTED)
         nk = dec_selected_keys(p, b, g, key0, t1 * C::BK);
       else
-        nk = min(p.chunk, L - key0);
+        nk = min(chunk, L - key0);
       const int n_tiles = (nk + C::BK - 1) / C::BK;
       if constexpr (PAGED) {
         // Tile keys [kt, kt + 64) of request b come from `per` cache blocks: one box per block
@@ -390,16 +405,16 @@ __global__ void __launch_bounds__(160, 1)
       const int hb = static_cast<int>(item - static_cast<long long>(cid) * p.n_hb);
       int b = cid, c = 0;
       if constexpr (MODE != DEC_SELECTED) {
-        dec_find_chunk(p.cu_k, p.n_seqs, p.chunk, cid, b, c);
+        dec_find_chunk(p.cu_k, p.n_seqs, chunk, cid, b, c);
         if (b < 0) break;
       }
       const int L = dec_ld<MODE>(p.cu_k + b + 1) - dec_ld<MODE>(p.cu_k + b);
-      const int key0 = MODE == DEC_SELECTED ? t0 * C::BK : c * p.chunk;
+      const int key0 = MODE == DEC_SELECTED ? t0 * C::BK : c * chunk;
       int nk;
       if constexpr (MODE == DEC_SELECTED)
         nk = dec_selected_keys(p, b, (hb * p.RB) / p.R, key0, t1 * C::BK);
       else
-        nk = min(p.chunk, L - key0);
+        nk = min(chunk, L - key0);
       const int n_tiles = (nk + C::BK - 1) / C::BK;
       const int pos = L - 1;  // the query is the newest token of its request
       // q fragments: rows g8 and g8+8 are heads hb*RB + row (zero when row >= RB).
@@ -690,14 +705,15 @@ __device__ __forceinline__ void dec_merge(const DecParams& p, int b, int g) {
   __shared__ int s_start;
   __shared__ float s_m[64], s_z[64];
   const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
+  const int chunk = dec_chunk(p);
   if (threadIdx.x < 32) {
-    const int st = dec_chunk_start(p.cu_k, b, p.chunk);
+    const int st = dec_chunk_start(p.cu_k, b, chunk);
     if (threadIdx.x == 0) s_start = st;
   }
   __syncthreads();
   const int c0 = s_start;
   // (never past the workspace, should the key counts exceed the bound they were sized by)
-  const int n = min((L + p.chunk - 1) / p.chunk, p.n_slots - c0);
+  const int n = min((L + chunk - 1) / chunk, p.n_slots - c0);
   using OutT = typename std::conditional<BF16, __nv_bfloat16, __half>::type;
   OutT* out = reinterpret_cast<OutT*>(p.out);
   for (int rb = 0; rb < p.R; rb += 64) {  // heads of the group, 64 at a time

@@ -636,6 +636,7 @@ int mea_decode_paged(const void* q, const void* k_cache, const void* v_cache,
   p.n_hb = n_heads_q / p.RB;
   p.chunk = L.chunk;
   p.n_slots = L.n_slots;
+  p.may_exceed = static_cast<long long>(n_seqs) * max_seqlen_k > total_k;
   p.n_items = static_cast<long long>(L.n_slots) * p.n_hb;
   p.c1 = scale * 1.4426950408889634f;
   p.timeout_ns = g_timeout_ns.load();

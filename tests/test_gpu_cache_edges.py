@@ -55,3 +55,41 @@ def test_lists_and_queries_rewritten_between_calls(n, length):
     for a, b in zip(run(torch.cuda.synchronize), run(lambda: None)):
         assert torch.equal(a, b)
     assert mea.device_error() == 0
+
+
+# -------------------------------------------------------------------------- requests sharing blocks
+def shared_cache(lens, hq, hkv, d, dtype, bs, seed, extra):
+    """Requests that all read the blocks of the longest one, from its first on."""
+    c = ref.Cache([max(lens)], hq, hkv, d, dtype, bs, seed, extra=extra)
+    c.lens = lens
+    c.k, c.v = [c.k[0][:n] for n in lens], [c.v[0][:n] for n in lens]
+    c.table, c.cu = c.table.expand(len(lens), -1).contiguous(), cu_seqlens(lens)
+    return c
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d,dtype,bs,split,alibi", [
+    ([1200, 1200, 960], 8, 2, 64, BF, 16, 0, False),
+    ([1200, 1200, 960], 8, 2, 64, BF, 16, 64, True),
+    ([800] * 50 + [1, 0, 799], 16, 2, 128, FP, 32, 128, False),   # fifty times the cache's slots
+    ([3000, 2999, 17, 3000], 40, 2, 128, BF, 64, 0, True),
+    ([500, 500], 4, 4, 256, FP, 16, 64, False),
+])
+def test_decode_paged_over_shared_blocks(lens, hq, hkv, d, dtype, bs, split, alibi):
+    """Without a bound on the keys the workspace is sized by the cache's slots: the requests together
+    hold more keys than that, and all of them count."""
+    c = shared_cache(lens, hq, hkv, d, dtype, bs, 141, extra=1)
+    assert sum(lens) > c.num_blocks * bs
+    q = randn((len(lens), hq, d), 142, dtype)
+    slopes = alibi_slope_values(hq) if alibi else None
+    kc, vc, table, cu = c.gpu()
+    gs = None if slopes is None else slopes.cuda()
+    o, m, z, _ = ref.decode(c, q, d ** -0.5, slopes)
+    size = mea.decode_workspace_size(len(lens), c.num_blocks * bs, hq, hkv, d, split)
+    ws = torch.zeros(size + 4096, dtype=torch.uint8, device="cuda")
+    ws[size:] = 77
+    for kw in ({}, {"workspace": ws[:size]}, {"total_k_bound": sum(lens)}):
+        out, lse = mea.decode_paged(q.cuda(), kc, vc, table, cu, max(lens), alibi_slopes=gs,
+                                    scale=d ** -0.5, split_keys=split, **kw)
+        ref.check_out(out.cpu(), lse.cpu(), o, m, z, dtype)
+    assert bool((ws[size:] == 77).all())
+    assert mea.device_error() == 0
