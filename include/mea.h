@@ -370,8 +370,10 @@ int mea_attention_weights(const void* q, const void* k, const float* lse,
  *                block is named twice.
  *                Slots past the kept keys are left as they were.
  *   kept         DEVICE int32 [n_seqs, n_heads_kv, n_keep]: the kept keys' indices, ascending, then -1.
- *   out_weights  DEVICE fp32 [n_seqs, n_heads_kv, n_keep]: the kept keys' weights, then 0. Not weights.
+ *   out_weights  DEVICE fp32 [n_seqs, n_heads_kv, n_keep]: the kept keys' weights, then 0.
  *   out_cu_seqlens_k  DEVICE int32 [n_seqs + 1]: prefix sums of min(L_b, n_keep).
+ * kept, out_weights and out_cu_seqlens_k overlap neither each other nor weights, cu_seqlens_k or the
+ * tables (MEA_ERR_SHAPE): lengths and weights are not updated in place.
  * Different heads keep different keys: afterwards slot t of a request holds another token's key for
  * each head, so a position-dependent bias (ALiBi) no longer applies to the new cache.
  */

@@ -752,7 +752,8 @@ def evict_paged(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch
     are blocks of ``out_k_cache`` / ``out_v_cache`` (None: of the same caches, and then none that a
     request still reads from). Returns ``(kept [n_seqs, Hkv, n_keep] int32, out_weights of the same
     shape, out_cu_seqlens_k [n_seqs + 1])``: the kept keys' indices (then -1) and weights (then 0)
-    and the new prefix sums. Afterwards a slot holds another token's key for each head, so ALiBi no
+    and the new prefix sums, in buffers other than the inputs' (lengths and weights are not updated
+    in place). Afterwards a slot holds another token's key for each head, so ALiBi no
     longer applies."""
     idx, (nb, bs, hkv, d), code, table, cu = _check_paged(k_cache, v_cache, block_table,
                                                           cu_seqlens_k)

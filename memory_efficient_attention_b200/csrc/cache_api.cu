@@ -29,6 +29,12 @@ __attribute__((visibility("hidden"))) int device_error(unsigned int* code, bool 
 
 namespace {
 
+// Whether two buffers of 32-bit elements share a byte.
+bool overlap(const void* a, long long na, const void* b, long long nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y + 4 * static_cast<uintptr_t>(nb) && y < x + 4 * static_cast<uintptr_t>(na);
+}
+
 bool block_size_ok(int bs) { return bs == 16 || bs == 32 || (bs >= 64 && bs % 64 == 0); }
 
 // The checks that every operator on the cache shares, in the order of the statuses' documentation.
@@ -398,6 +404,25 @@ int mea_evict_paged(const void* k_cache, const void* v_cache, const int32_t* blo
       !aligned(cu_seqlens_k, 4) || !aligned(weights, 4) || !aligned(out_weights, 4) ||
       !aligned(kept, 4) || !aligned(out_cu_seqlens_k, 4))
     return MEA_ERR_ALIGN;
+  // CTAs read lengths, weights and tables while others write the new ones: no updates in place.
+  {
+    struct Span {
+      const void* at;
+      long long n;
+    };
+    const Span outs[] = {
+        {kept, pairs * n_keep}, {out_weights, pairs * n_keep}, {out_cu_seqlens_k, n_seqs + 1ll}};
+    const Span ins[] = {{weights, pairs * weights_stride},
+                        {cu_seqlens_k, n_seqs + 1ll},
+                        {block_table, static_cast<long long>(n_seqs) * max_blocks},
+                        {out_table, static_cast<long long>(n_seqs) * max_out_blocks}};
+    for (int i = 0; i < 3; ++i) {
+      for (const Span& in : ins)
+        if (overlap(outs[i].at, outs[i].n, in.at, in.n)) return MEA_ERR_SHAPE;
+      for (int j = 0; j < i; ++j)
+        if (overlap(outs[i].at, outs[i].n, outs[j].at, outs[j].n)) return MEA_ERR_SHAPE;
+    }
+  }
   DeviceInfo di;
   if (int rc = current_device_info(di); rc != MEA_OK) return rc;
   mea::EvictParams p{};

@@ -93,3 +93,22 @@ def test_decode_paged_over_shared_blocks(lens, hq, hkv, d, dtype, bs, split, ali
         ref.check_out(out.cpu(), lse.cpu(), o, m, z, dtype)
     assert bool((ws[size:] == 77).all())
     assert mea.device_error() == 0
+
+
+# ---------------------------------------------------------------------------- outputs over inputs
+def test_eviction_refuses_updates_in_place():
+    """The new lengths over the old ones, the kept weights over the weights: refused, and nothing
+    written."""
+    c = ref.Cache([64, 48], 2, 2, 64, BF, 16, 161)
+    kc, vc, table, cu = c.gpu()
+    w = randn((2, 2, 64), 162, torch.float32, "cuda")
+    ot = torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    ko = torch.zeros((4, 16, 2, 64), dtype=BF, device="cuda")
+    before = (cu.clone(), w.clone())
+    for kw in ({"out_cu_seqlens_k": cu}, {"out_weights": w.view(-1)[:64].view(2, 2, 16)}):
+        with pytest.raises(mea.MeaError) as e:
+            mea.evict_paged(kc, vc, table, cu, 64, w, 16, 2, ot, out_k_cache=ko,
+                            out_v_cache=ko.clone(), **kw)
+        assert e.value.rc == mea._lib.MEA_ERR_SHAPE
+    torch.cuda.synchronize()
+    assert torch.equal(cu, before[0]) and torch.equal(w, before[1]) and not bool(ko.any())
