@@ -322,7 +322,8 @@ int mea_decode_selected(const void* q, const void* k_cache, const void* v_cache,
  *   weights[b, g, t] = prev_weights[b, g, t] + sum over h in group g of exp(score_ht - lse_h)
  * for 0 <= t < L_b; entries from L_b on are left as they were.
  *   weights, prev_weights  DEVICE fp32 [n_seqs, n_heads_kv, weights_stride], weights_stride >=
- *                          max_seqlen_k; prev_weights may be NULL (zeros) or weights itself.
+ *                          max_seqlen_k; prev_weights may be NULL (zeros) or weights itself, and
+ *                          does not overlap it otherwise (MEA_ERR_SHAPE).
  *   workspace  at least mea_decode_weights_workspace_size(...) bytes, 256-byte aligned (the decode's
  *              partials and one fp32 score per key and query head).
  * total_k and split_keys as for mea_decode_paged; n_seqs <= 65535, n_heads_kv <= 65535.

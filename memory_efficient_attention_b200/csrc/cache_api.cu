@@ -347,6 +347,11 @@ int mea_decode_weights(const void* q, const void* k_cache, const void* v_cache,
       !aligned(weights, 4) || (prev_weights && !aligned(prev_weights, 4)) ||
       (alibi_slopes && !aligned(alibi_slopes, 4)))
     return MEA_ERR_ALIGN;
+  // (The same tensor is read and written element by element; a shifted one would be read too late.)
+  const long long n_weights = static_cast<long long>(n_seqs) * n_heads_kv * weights_stride;
+  if (prev_weights && prev_weights != weights &&
+      overlap(prev_weights, n_weights, weights, n_weights))
+    return MEA_ERR_SHAPE;
   if (!workspace || !aligned(workspace, 256)) return MEA_ERR_WORKSPACE;
   DeviceInfo di;
   if (int rc = current_device_info(di); rc != MEA_OK) return rc;
