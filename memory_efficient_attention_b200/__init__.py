@@ -405,8 +405,9 @@ def decode_splitkv_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
 # ------------------------------------------------------------------------------------------
 # These checks run before every decode step's launches, whose kernels can be as short as the checks:
 # they compare device indices and shapes directly and copy nothing that fits already.
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_cur_device = torch._C._cuda_getDevice
+# (A torch without CUDA has neither function, nor a GPU tensor that would reach them.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_cur_device = getattr(torch._C, "_cuda_getDevice", None)
 _INV_SQRT: dict = {}  # head dim -> 1 / sqrt
 _DTYPE_CODES = {torch.float16: _lib.MEA_F16, torch.bfloat16: _lib.MEA_BF16}
 
