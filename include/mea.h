@@ -255,11 +255,12 @@ int mea_decode_paged(const void* q, const void* k_cache, const void* v_cache,
  * MEA_F16 or MEA_BF16, block_size 16, 32 or a multiple of 64, block_table DEVICE int32
  * [n_seqs, max_blocks], cu_seqlens_k DEVICE int32 [n_seqs + 1] prefix sums of the requests' key
  * counts L_b, max_seqlen_k an upper bound on every L_b with max_blocks * block_size >=
- * max_seqlen_k, D a multiple of 8 from 8 to 256. A block id outside [0, num_blocks) reads as zeros, and
- * nothing is written for it (neither faults). Slots past a request's end may hold any bits. No
- * atomics on results: every result is deterministic. None of the calls allocates device memory or
- * synchronises the host, and all can be captured into a CUDA graph; two calls that may run at
- * the same time (two streams, two graphs) need a workspace each.
+ * max_seqlen_k, D a multiple of 8 from 8 to 256. A block id outside [0, num_blocks) reads as zeros,
+ * and nothing is written for it (neither faults). Slots past a request's end may hold any bits.
+ * Where max_seqlen_k is 0 (requests without keys) weights may be NULL. No atomics on results: every
+ * result is deterministic. None of the calls allocates device memory or synchronises the host, and
+ * all can be captured into a CUDA graph; two calls that may run at the same time (two streams, two
+ * graphs) need a workspace each.
  */
 
 /* Blocks per request that mea_select_blocks can choose from. */

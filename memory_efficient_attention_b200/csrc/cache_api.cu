@@ -79,9 +79,13 @@ int launch_split(const CUtensorMap& tk, const CUtensorMap& tv, const mea::DecPar
       return MEA_ERR_CUDA;
     return MEA_OK;
   } else {
-    if (grid > 0) kern<<<grid, threads, smem, stream>>>(tk, tv, p);
-    if (cudaGetLastError() != cudaSuccess) return MEA_ERR_CUDA;
     const dim3 wgrid(1 + (max_seqlen_k + 1023) / 1024, p.hq / p.R, p.n_seqs);
+    if (grid == 0) {  // no keys at all: nothing of ours runs before the merge
+      mea::mea_decode_weights_kernel<D, BF16><<<wgrid, 256, 0, stream>>>(p);
+      return cudaGetLastError() == cudaSuccess ? MEA_OK : MEA_ERR_CUDA;
+    }
+    kern<<<grid, threads, smem, stream>>>(tk, tv, p);
+    if (cudaGetLastError() != cudaSuccess) return MEA_ERR_CUDA;
     return launch_dependent(mea::mea_decode_weights_kernel<D, BF16>, wgrid, 256, 0, stream, p) ==
                    cudaSuccess
                ? MEA_OK
@@ -331,7 +335,8 @@ int mea_decode_weights(const void* q, const void* k_cache, const void* v_cache,
                        int n_heads_kv, int head_dim, float scale, const float* alibi_slopes,
                        int dtype, void* workspace, size_t workspace_bytes, int split_keys,
                        void* stream) {
-  if (!q || !k_cache || !v_cache || !block_table || !cu_seqlens_k || !out || !weights)
+  if (!q || !k_cache || !v_cache || !block_table || !cu_seqlens_k || !out ||
+      (max_seqlen_k > 0 && !weights))
     return MEA_ERR_NULL;
   if (int rc = check_cache(n_seqs, num_blocks, block_size, max_blocks, n_heads_kv, head_dim, dtype))
     return rc;
@@ -389,8 +394,8 @@ int mea_evict_paged(const void* k_cache, const void* v_cache, const int32_t* blo
                     int num_out_blocks, int block_size, int max_blocks, int max_out_blocks,
                     int max_seqlen_k, int n_heads_kv, int head_dim, int n_keep, int n_recent,
                     int dtype, void* stream) {
-  if (!k_cache || !v_cache || !block_table || !cu_seqlens_k || !weights || !out_k_cache ||
-      !out_v_cache || !out_table || !kept || !out_weights || !out_cu_seqlens_k)
+  if (!k_cache || !v_cache || !block_table || !cu_seqlens_k ||
+      (max_seqlen_k > 0 && !weights) || !out_k_cache || !out_v_cache || !out_table || !kept || !out_weights || !out_cu_seqlens_k)
     return MEA_ERR_NULL;
   if (int rc = check_cache(n_seqs, num_blocks, block_size, max_blocks, n_heads_kv, head_dim, dtype))
     return rc;

@@ -112,3 +112,39 @@ def test_eviction_refuses_updates_in_place():
         assert e.value.rc == mea._lib.MEA_ERR_SHAPE
     torch.cuda.synchronize()
     assert torch.equal(cu, before[0]) and torch.equal(w, before[1]) and not bool(ko.any())
+
+
+# ---------------------------------------------------------------------------------------- no keys
+def test_requests_without_any_keys():
+    """A batch before its first token: outputs of rows that attend to nothing, no weights, no keys."""
+    n, hq, hkv, d, bs = 3, 4, 2, 64, 16
+    dev = {"device": "cuda"}
+    kc = torch.full((4, bs, hkv, d), math.nan, dtype=BF, **dev)
+    table = torch.full((n, 2), 1 << 30, dtype=torch.int32, **dev)
+    cu, q = torch.zeros(n + 1, dtype=torch.int32, **dev), randn((n, hq, d), 171, BF, "cuda")
+    w = torch.empty((n, hkv, 0), **dev)
+    for prev in (None, w):
+        out, lse, _ = mea.decode_paged_weights(q, kc, kc, table, cu, 0, w, prev_weights=prev)
+        assert not bool(out.any()) and bool((lse == -math.inf).all())
+    ko = torch.zeros((n, bs, hkv, d), dtype=BF, **dev)
+    vo = torch.zeros_like(ko)
+    ids = torch.arange(n, dtype=torch.int32, **dev).view(n, 1)
+    kept, ow, ocu = mea.evict_paged(kc, kc, table, cu, 0, w, 8, 2, ids, out_k_cache=ko,
+                                    out_v_cache=vo)
+    assert bool((kept == -1).all()) and not bool(ow.any()) and not bool(ocu.any())
+    assert not bool(ko.any()) and not bool(vo.any())
+    sel = mea.select_blocks(q, torch.zeros((4, hkv, 2, d), dtype=BF, **dev), table, cu, 0, bs, 3)
+    assert bool((sel == -1).all())
+    mea.block_key_bounds(kc, table, cu, 0)
+    for out, lse in (mea.decode_paged_selected(q, kc, kc, table, cu, sel),
+                     mea.decode_paged(q, kc, kc, table, cu, 0),
+                     mea.decode_tree_paged(q, kc, kc, table, cu, cu, 1, 0,
+                                           torch.ones((n, 1), dtype=torch.int32, **dev),
+                                           out=torch.zeros_like(q),
+                                           lse=torch.full((hq, n), -math.inf, **dev))):
+        assert not bool(out.any()) and bool((lse == -math.inf).all())
+    none = torch.empty((0, hkv, d), dtype=BF, **dev)
+    got = mea.attention_packed_weights(torch.empty((0, hq, d), dtype=BF, **dev), none,
+                                       torch.empty((hq, 0), **dev), cu, cu, 0, 0)
+    assert got.shape == (n, hkv, 0)
+    assert mea.device_error() == 0
