@@ -66,8 +66,12 @@ struct WeightsCfg {
   static constexpr int NQ = D == 64 ? 4 : 2;     // Q tiles in the ring
   static constexpr uint32_t SMEM_K = 0;
   static constexpr uint32_t SMEM_Q = NK * SUBS * TILE_BYTES;
-  static constexpr uint32_t SMEM_T = SMEM_Q + NQ * TILE_BYTES;   // 2 NBUF x 3 x 128 floats
-  static constexpr uint32_t SMEM_SUM = SMEM_T + 2 * NBUF * 3 * 512;  // 3 warpgroups x 128 floats
+  // Column terms, 2 NBUF slots: nl[128], and with ALiBi slopes[128] and (not causal) positions[128];
+  // under a causal mask one such nl, slopes for every 32 keys.
+  static constexpr int GROUPS = KT / 32;
+  static constexpr int SLOT = GROUPS * 256;  // floats
+  static constexpr uint32_t SMEM_T = SMEM_Q + NQ * TILE_BYTES;
+  static constexpr uint32_t SMEM_SUM = SMEM_T + 2 * NBUF * SLOT * 4;  // 3 warpgroups x 128 floats
   static constexpr uint32_t SMEM_MISC = SMEM_SUM + 3 * 512;
   static constexpr int QD = 4;                   // ranges in the queue, 64 bytes each
   static constexpr uint32_t MISC_QUEUE = 256;
@@ -249,8 +253,8 @@ struct WeightsWalk {
 };
 
 // Adds 2^score over 32 columns of one key to acc. x: the raw products; terms: shared memory, this
-// chunk's row terms (nl, and with ALiBi the slopes and, non-causal, the queries' positions); key: the
-// key's index in the item. EDGE: only the columns whose bit of `live` is set count.
+// chunk's column terms (nl, and with ALiBi the slopes and, non-causal, the queries' positions); key:
+// the key's index in the item (causal: from the middle of its warp's 32). EDGE: only the columns whose bit of `live` is set count.
 template <bool CAUSAL, bool ALIBI, bool EDGE>
 __device__ __forceinline__ void weights_chunk(const uint32_t (&x)[32], const float* terms,
                                               uint64_t c1x2, float key, uint32_t live,
@@ -475,8 +479,13 @@ __global__ void __launch_bounds__(640, 1)
     __syncwarp();
   } else if (warp == 18) {
     // ---------------------------------------------------------------- column terms
-    //   nl[c] = -lse2 (causal ALiBi: - slope2 (p_c - j0) as well: with the key's own + slope2 key the
-    //   terms stay small where weights are not), sl[c] = slope2, ps[c] = p_c - j0.
+    //   nl[c] = -lse2, sl[c] = slope2, ps[c] = p_c - j0. Under a causal mask the distance term is
+    //   split, slope2 (key - m) - slope2 (p_c - m), and its second half added here, so that a thread
+    //   loads two terms a column and not three (the loads take as long as the exponentials then: 32.4
+    //   us instead of 27.7 for the last 32 queries of 16 prompts). m is the middle of the 32 keys of
+    //   the key's warp: where a weight counts, both halves are within slope2 * 16 of the whole, and
+    //   so is their rounding. (With m the item's first key, up to 255 slope2 away, weights were off
+    //   by 2e-4 under slopes of 16.)
     uint32_t n_frag = 0, k = 0;
     while (volatile WeightsEntry* e = range(n_frag, true)) {
       const int g = e->g, q0 = e->q0, lq = e->lq, qbeg = e->qbeg, nt = e->nt;
@@ -490,7 +499,7 @@ __global__ void __launch_bounds__(640, 1)
         float nl[4], sl[4], ps[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int c = u * 32 + lane;
+          const int c = 4 * lane + u;
           const int i = qbeg + t * (128 >> p.log2_p) + (c >> p.log2_p);
           const int head = g * p.R + (hb << p.log2_p) + (c & ((1 << p.log2_p) - 1));
           nl[u] = -INFINITY;
@@ -501,7 +510,6 @@ __global__ void __launch_bounds__(640, 1)
             if constexpr (ALIBI) {
               sl[u] = __ldg(p.slopes + head) * LOG2E;
               ps[u] = static_cast<float>(i + pos0);
-              if (CAUSAL) nl[u] -= sl[u] * ps[u];
             }
           }
         }
@@ -510,13 +518,24 @@ __global__ void __launch_bounds__(640, 1)
                          ecode | 6);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        float* dst =
-            reinterpret_cast<float*>(smem + C::SMEM_T) + (k % (2 * C::NBUF)) * 384 + lane;
+        float4* dst = reinterpret_cast<float4*>(smem + C::SMEM_T) +
+                      (k % (2 * C::NBUF)) * (C::SLOT / 4) + lane;
+        if constexpr (ALIBI && CAUSAL) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          dst[u * 32] = nl[u];
-          if constexpr (ALIBI) dst[128 + u * 32] = sl[u];
-          if constexpr (ALIBI && !CAUSAL) dst[256 + u * 32] = ps[u];
+          for (int m = 0; m < C::GROUPS; ++m) {
+            const float mid = m * 32 + 16;
+            dst[m * 64] = make_float4(fmaf(-sl[0], ps[0] - mid, nl[0]),
+                                      fmaf(-sl[1], ps[1] - mid, nl[1]),
+                                      fmaf(-sl[2], ps[2] - mid, nl[2]),
+                                      fmaf(-sl[3], ps[3] - mid, nl[3]));
+            dst[m * 64 + 32] = make_float4(sl[0], sl[1], sl[2], sl[3]);
+          }
+        } else {
+          dst[0] = make_float4(nl[0], nl[1], nl[2], nl[3]);
+          if constexpr (ALIBI) {
+            dst[32] = make_float4(sl[0], sl[1], sl[2], sl[3]);
+            dst[64] = make_float4(ps[0], ps[1], ps[2], ps[3]);
+          }
         }
         __syncwarp();
         if (lane < C::SUBS) mbar_arrive(BAR(B_SF + b * C::SUBS + lane));
@@ -565,12 +584,13 @@ __global__ void __launch_bounds__(640, 1)
     const int r = threadIdx.x & 127;
     const uint32_t t_s = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) +
                          (buf * C::SUBS + h) * 128;
-    // This warpgroup's column terms: two slots per buffer, in turn.
-    const float* terms0 = reinterpret_cast<const float*>(smem + C::SMEM_T) + buf * 384;
+    // This warp's column terms: two slots per buffer, in turn.
+    const float* terms0 = reinterpret_cast<const float*>(smem + C::SMEM_T) + buf * C::SLOT +
+                          (ALIBI && CAUSAL ? (h * 4 + (warp & 3)) * 256 : 0);
     int slot = 0;
     const uint32_t bar_f = BAR(B_SF + wg), bar_e = BAR(B_SE + wg);  // (wg = buf * SUBS + h)
     const uint64_t c1x2 = f2_pack(p.c1, p.c1);
-    const float key = static_cast<float>(h * 128 + r);
+    const float key = static_cast<float>(CAUSAL ? lane - 16 : h * 128 + r);
     float* sums = reinterpret_cast<float*>(smem + C::SMEM_SUM);
     uint32_t n_frag = 0, n_join = 0, phase = 0;
     int ahead = buf;  // steps until this warpgroup's next one
@@ -596,7 +616,7 @@ __global__ void __launch_bounds__(640, 1)
         if (!ok) break;
         phase ^= 1u;
         const float* terms = terms0 + slot;
-        slot = C::NBUF * 384 - slot;
+        slot = C::NBUF * C::SLOT - slot;
         tc_fence_after();
         uint64_t acc[4] = {0ull, 0ull, 0ull, 0ull};
         // 32 columns at a time; once the last ones are in registers the buffer is free, and the next

@@ -148,3 +148,26 @@ def test_requests_without_any_keys():
                                        torch.empty((hq, 0), **dev), cu, cu, 0, 0)
     assert got.shape == (n, hkv, 0)
     assert mea.device_error() == 0
+
+
+# ------------------------------------------------------------------------------- prompt's weights
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("d", [64, 256])
+def test_prompt_weights_under_steep_slopes(d, causal):
+    """Slopes under which distance terms are thousands of times the scores. The kernel's terms stay
+    within 16.3 log2(e) * 16 = 376 of a counting weight's exponent: three roundings of values below
+    512, half a step each, make 3 * 2^-16 ln 2 = 3.2e-5 at most, below the fp32 bound of 2^-14."""
+    lens, hq, hkv = [700, 333], 4, 2
+    q, k, v = make_qkv(lens, lens, hq, hkv, d, BF, 151)
+    slopes = torch.tensor([16.3, 0.7, 5.1, 2.9])
+    cu = cu_seqlens(lens)
+    _, lse = mea.attention_packed(q.cuda(), k.cuda(), v.cuda(), cu.cuda(), cu.cuda(), 700,
+                                  causal=causal, alibi_slopes=slopes.cuda(), scale=d ** -0.5)
+    got = mea.attention_packed_weights(q.cuda(), k.cuda(), lse, cu.cuda(), cu.cuda(), 700, 700,
+                                       causal=causal, alibi_slopes=slopes.cuda(),
+                                       scale=d ** -0.5).cpu()
+    want = ref.prompt_weights(q, k, lse.cpu(), lens, lens, d ** -0.5, causal, slopes, 0, 700)
+    for s, n in enumerate(lens):
+        e = (got[s, :, :n].double() - want[s, :, :n]).abs()
+        bound = ref.F32 * want[s, :, :n] + 1e-30
+        assert bool((e <= bound).all()), float((e / bound).max())
