@@ -609,7 +609,7 @@ __global__ void __launch_bounds__(640, 1)
         t += C::NBUF;
         while (t >= nt) t -= nt;
         // Columns [lo, hi) count for this key; every key of the tile sees all 128 off the edges.
-        const int hi = (left - qi) << p.log2_p;
+        const int hi = min(left - qi, 128) << p.log2_p;
         const bool edge = hi < 128 || (CAUSAL && qi < j + 127);
         ok = mbar_wait(bar_f, phase, abort_flag, tmo, ecode | 8);
         ok = __all_sync(0xffffffffu, ok);

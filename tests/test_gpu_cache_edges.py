@@ -171,3 +171,19 @@ def test_prompt_weights_under_steep_slopes(d, causal):
         e = (got[s, :, :n].double() - want[s, :, :n]).abs()
         bound = ref.F32 * want[s, :, :n] + 1e-30
         assert bool((e <= bound).all()), float((e / bound).max())
+
+
+def test_prompt_weights_of_more_columns_than_an_int_counts():
+    """2^25 queries of 128 heads on one KV head are 2^32 (query, head) columns: each adds
+    exp(0 - 0) = 1 to every key's weight (86 GB of zeros)."""
+    lq, hq, d, lk = 1 << 25, 128, 8, 130
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GB")
+    q = torch.zeros((lq, hq, d), dtype=BF, device="cuda")
+    lse = torch.zeros((hq, lq), device="cuda")
+    k = torch.zeros((lk, 1, d), dtype=BF, device="cuda")
+    w = mea.attention_packed_weights(q, k, lse, cu_seqlens([lq]).cuda(), cu_seqlens([lk]).cuda(),
+                                     lq, lk).cpu()
+    # (whole numbers: only the fp32 additions of the partial sums, up to 2^32, round)
+    assert float((w.double() / (lq * hq) - 1).abs().max()) <= 148 * 2.0 ** -24
+    assert mea.device_error() == 0
