@@ -187,3 +187,93 @@ def test_prompt_weights_of_more_columns_than_an_int_counts():
     # (whole numbers: only the fp32 additions of the partial sums, up to 2^32, round)
     assert float((w.double() / (lq * hq) - 1).abs().max()) <= 148 * 2.0 ** -24
     assert mea.device_error() == 0
+
+
+def steps_of(lens_q, lens_k, hq, hkv, d, causal, last, sms=148):
+    """The kernel's schedule by its definition: steps per item of one head block, head blocks, and
+    the equal ranges that the CTAs take."""
+    r = hq // hkv
+    p = 1
+    while p < 128 and r % (2 * p) == 0:
+        p *= 2
+    kt, qt = (128 if d > 128 else 256), 128 // p
+    items = []  # (Q tiles, head blocks) in the order of the line
+    for lq, lk in zip(lens_q, lens_k):
+        qw = max(0, lq - last) if last else 0
+        for _ in range(hkv):
+            for j in range(0, lk, kt):
+                first = max(qw, j - (lk - lq)) if causal else qw
+                items.append((max(-(-(lq - first) // qt), 1), r // p))
+    total = sum(n * h for n, h in items)
+    # (the host's bound on the steps sizes the grid)
+    bound = len(lens_q) * hkv * -(-max(lens_k) // kt) * (r // p) * (-(-max(lens_q) // qt) + 1)
+    return items, total, -(-total // min(bound, sms))
+
+
+def prompt_weights_gpu(q, k, lse, lens_q, lens_k, scale, causal, slopes, last, width):
+    """cache_reference.prompt_weights in 64 bits on the GPU, some rows at a time."""
+    hq, hkv = q.shape[1], k.shape[1]
+    out = torch.zeros(len(lens_q), hkv, width, dtype=torch.float64, device="cuda")
+    qo = ko = 0
+    for s, (lq, lk) in enumerate(zip(lens_q, lens_k)):
+        j = torch.arange(lk, device="cuda")
+        for i0 in range(max(0, lq - last) if last else 0, lq, 1024):
+            i = torch.arange(i0, min(lq, i0 + 1024), device="cuda")
+            pos = i + lk - lq
+            for h in range(hq):
+                x = scale * (q[qo + i, h].double() @ k[ko:ko + lk, h // (hq // hkv)].double().t())
+                if slopes is not None:
+                    x -= float(slopes[h]) * (pos[:, None] - j).abs()
+                x -= lse[h, qo + i, None].double()
+                if causal:
+                    x.masked_fill_(j[None, :] > pos[:, None], -math.inf)
+                out[s, h // (hq // hkv), :lk] += torch.exp(x).sum(0)
+        qo += lq
+        ko += lk
+    return out.cpu()
+
+
+@pytest.mark.parametrize("lens_q,lens_k,hq,hkv,d,dtype,causal,alibi,last", [
+    ([3000, 2100, 5], [3000, 2100, 5], 16, 8, 64, BF, True, True, 0),
+    ([3000, 2100, 5], [3000, 2100, 5], 16, 8, 128, BF, True, False, 0),
+    ([3000, 2100, 5], [3000, 2100, 5], 16, 8, 128, FP, False, True, 0),
+    ([2500, 130], [1700, 4000], 24, 2, 128, BF, True, True, 0),     # 12 heads a group: 3 blocks of 4
+    ([1500, 0, 900], [2200, 300, 900], 36, 4, 80, FP, False, False, 0),  # 9 heads: 9 blocks of 1
+    ([2600, 700], [2600, 700], 16, 4, 256, BF, True, True, 0),      # four score buffers
+    ([1800, 999], [1800, 999], 12, 2, 200, FP, False, False, 0),
+    ([200, 137, 256, 64] * 60, [200, 137, 256, 64] * 60, 8, 4, 64, BF, True, False, 0),
+    ([600, 300] * 20, [2000, 1100] * 20, 32, 8, 128, BF, True, True, 100),
+])
+def test_prompt_weights_of_many_steps_a_cta(lens_q, lens_k, hq, hkv, d, dtype, causal, alibi, last):
+    """Ranges of many steps: the join of the warpgroups, rings and queues that come round several
+    times, items begun by one CTA and ended by another, head blocks that follow each other."""
+    items, total, per = steps_of(lens_q, lens_k, hq, hkv, d, causal, last)
+    nbuf = 4 if d > 128 else 2
+    assert per > 2 * nbuf
+    if items[0][1] > 1:  # a CTA's range crosses from one head block of an item to the next
+        at, crossed = 0, False
+        for n, hb in items:
+            crossed |= any((at + n * b) % per for b in range(1, hb))
+            at += n * hb
+        assert crossed
+    q, k, v = make_qkv(lens_q, lens_k, hq, hkv, d, dtype, 181)
+    slopes = alibi_slope_values(hq) if alibi else None
+    gs = None if slopes is None else slopes.cuda()
+    q, k, v, cq, ck = q.cuda(), k.cuda(), v.cuda(), cu_seqlens(lens_q).cuda(), \
+        cu_seqlens(lens_k).cuda()
+    _, lse = mea.attention_packed(q, k, v, cq, ck, max(lens_q), causal=causal, alibi_slopes=gs,
+                                  scale=d ** -0.5)
+    width = max(lens_k) + 3
+    w = torch.full((len(lens_q), hkv, width), 7.0, device="cuda")
+    run = lambda: mea.attention_packed_weights(  # noqa: E731
+        q, k, lse, cq, ck, max(lens_q), max(lens_k), causal=causal, alibi_slopes=gs,
+        scale=d ** -0.5, last_queries=last, weights=w).cpu()
+    got, again = run(), run()
+    assert torch.equal(got, again)
+    want = prompt_weights_gpu(q, k, lse, lens_q, lens_k, d ** -0.5, causal, slopes, last, width)
+    for s, lk in enumerate(lens_k):
+        e = (got[s, :, :lk].double() - want[s, :, :lk]).abs()
+        bound = ref.F32 * want[s, :, :lk] + 1e-30
+        assert bool((e <= bound).all()), float((e / bound).max())
+        assert bool((got[s, :, lk:] == 7).all())
+    assert mea.device_error() == 0
