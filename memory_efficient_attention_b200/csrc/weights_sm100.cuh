@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(640, 1)
     //   nl[c] = -lse2, sl[c] = slope2, ps[c] = p_c - j0. Under a causal mask the distance term is
     //   split, slope2 (key - m) - slope2 (p_c - m), and its second half added here, so that a thread
     //   loads two terms a column and not three (the loads take as long as the exponentials then: 32.4
-    //   us instead of 27.7 for the last 32 queries of 16 prompts). m is the middle of the 32 keys of
+    //   us instead of 27.9 for the last 32 queries of 16 prompts). m is the middle of the 32 keys of
     //   the key's warp: where a weight counts, both halves are within slope2 * 16 of the whole, and
     //   so is their rounding. (With m the item's first key, up to 255 slope2 away, weights were off
     //   by 2e-4 under slopes of 16.)
@@ -499,7 +499,8 @@ __global__ void __launch_bounds__(640, 1)
         float nl[4], sl[4], ps[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int c = 4 * lane + u;
+          // (where a table goes to every 32 keys, a lane has four columns next to each other)
+          const int c = ALIBI && CAUSAL ? 4 * lane + u : u * 32 + lane;
           const int i = qbeg + t * (128 >> p.log2_p) + (c >> p.log2_p);
           const int head = g * p.R + (hb << p.log2_p) + (c & ((1 << p.log2_p) - 1));
           nl[u] = -INFINITY;
@@ -518,23 +519,27 @@ __global__ void __launch_bounds__(640, 1)
                          ecode | 6);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        float4* dst = reinterpret_cast<float4*>(smem + C::SMEM_T) +
-                      (k % (2 * C::NBUF)) * (C::SLOT / 4) + lane;
+        float* dst = reinterpret_cast<float*>(smem + C::SMEM_T) + (k % (2 * C::NBUF)) * C::SLOT;
         if constexpr (ALIBI && CAUSAL) {
+          float4* dst4 = reinterpret_cast<float4*>(dst) + lane;
 #pragma unroll
           for (int m = 0; m < C::GROUPS; ++m) {
             const float mid = m * 32 + 16;
-            dst[m * 64] = make_float4(fmaf(-sl[0], ps[0] - mid, nl[0]),
+            dst4[m * 64] = make_float4(fmaf(-sl[0], ps[0] - mid, nl[0]),
                                       fmaf(-sl[1], ps[1] - mid, nl[1]),
                                       fmaf(-sl[2], ps[2] - mid, nl[2]),
                                       fmaf(-sl[3], ps[3] - mid, nl[3]));
-            dst[m * 64 + 32] = make_float4(sl[0], sl[1], sl[2], sl[3]);
+            dst4[m * 64 + 32] = make_float4(sl[0], sl[1], sl[2], sl[3]);
           }
         } else {
-          dst[0] = make_float4(nl[0], nl[1], nl[2], nl[3]);
-          if constexpr (ALIBI) {
-            dst[32] = make_float4(sl[0], sl[1], sl[2], sl[3]);
-            dst[64] = make_float4(ps[0], ps[1], ps[2], ps[3]);
+          dst += lane;
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            dst[u * 32] = nl[u];
+            if constexpr (ALIBI) {
+              dst[128 + u * 32] = sl[u];
+              dst[256 + u * 32] = ps[u];
+            }
           }
         }
         __syncwarp();
