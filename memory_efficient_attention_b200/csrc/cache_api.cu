@@ -226,6 +226,7 @@ int mea_select_blocks(const void* q, const void* bounds, const int32_t* block_ta
   p.n_last = n_last;
   p.n_seqs = n_seqs;
   p.max_live = static_cast<int>(live);
+  p.longest_first = n_seqs > 1 && n_seqs <= mea::kRankedSeqs && live >= 256;
   // CTAs per (request, head): as many as fill the SMs about twice, and no more than have a round of
   // 128 blocks to score.
   const long long pairs = static_cast<long long>(n_seqs) * n_heads_kv;
@@ -461,7 +462,8 @@ int mea_evict_paged(const void* k_cache, const void* v_cache, const int32_t* blo
   // Rank keys in shared memory for up to 48 Ki keys; longer rows are read again in every pass.
   constexpr int max_keys = 48 * 1024;
   p.smem_keys = max_seqlen_k < max_keys ? max_seqlen_k : max_keys;
-  p.longest_first = pairs > di.sms && n_seqs > 1 && n_seqs <= mea::kEvictThreads;
+  p.longest_first = pairs > di.sms && n_seqs > 1 && n_seqs <= mea::kRankedSeqs &&
+                    max_seqlen_k >= 4096;
   constexpr auto sel = mea::mea_evict_select_kernel;
   if (smem_attr_once<sel>(max_keys * 4) != cudaSuccess) return MEA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

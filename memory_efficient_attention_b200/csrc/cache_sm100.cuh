@@ -291,7 +291,13 @@ __device__ __forceinline__ uint32_t radix_select_wide(Get get, int n, int k, uin
 }
 
 // The request of rank `r` by length, longest first (equal ones by index), so that CTAs in rank order
-// leave no long request to the end. n <= the CTA's threads; len[n] and found[1] in shared memory.
+// leave no long request to the end. n <= kRankedSeqs; len[n] and found[1] in shared memory.
+// Every CTA counts for itself, n steps of n threads: worth it for few requests that can be long. With
+// it and without, on 8 KV heads: eviction of 64 requests of up to 16384 keys 85 and 90 us, of 32 of
+// 32768 56 and 60, but of 64 of 600 19.8 and 19.2, of 256 of 600 87 and 59, of 1024 of 600 1974 and
+// 225; block choice for 64 requests of up to 1024 blocks 38.5 and 42, of 256 20.3 and 20.5, of 128
+// 17.8 and 17.0, for 256 of 19 41 and 18.
+constexpr int kRankedSeqs = 64;
 __device__ __forceinline__ int nth_longest(const int32_t* cu, int n, int r, int* len, int* found) {
   const int t = threadIdx.x;
   int mine = 0;
@@ -374,6 +380,7 @@ struct SelectParams {
   int num_blocks, block_size, max_blocks, hq, hkv, dh, n_select, n_first, n_last;
   int n_seqs;
   int max_live;        // bound on a request's blocks: rank keys in shared memory
+  int longest_first;
 };
 
 constexpr int kSelThreads = 256;
@@ -409,7 +416,7 @@ __global__ void __launch_bounds__(kSelThreads, CHUNKS == 16 ? 1 : 2)
   const int g = pair % p.hkv;
   int b = pair / p.hkv;
   pdl_trigger();
-  if (p.n_seqs > 1 && p.n_seqs <= kSelThreads)
+  if (p.longest_first)
     b = nth_longest(p.cu_k, p.n_seqs, b, reinterpret_cast<int*>(s_w), s_sc.sum[0]);
   const int L = __ldg(p.cu_k + b + 1) - __ldg(p.cu_k + b);
   const int nblk = min((L + p.block_size - 1) / p.block_size, min(p.max_blocks, p.max_live));
@@ -651,7 +658,7 @@ __global__ void __launch_bounds__(kSelThreads, CHUNKS == 16 ? 1 : 2)
 // the others, those with the largest weights, n_keep in all, in ascending order. One CTA per
 // pair; the rank keys stay in shared memory when they fit. Bound by the passes over shared memory:
 // at up to 32768 keys one CTA fits an SM, and with more pairs than SMs the longest requests go first
-// (64 requests x 8 heads with the copy: 384 -> 378 us).
+// (nth_longest).
 // ------------------------------------------------------------------------------------------
 struct EvictParams {
   const void* k;

@@ -277,3 +277,47 @@ def test_prompt_weights_of_many_steps_a_cta(lens_q, lens_k, hq, hkv, d, dtype, c
         assert bool((e <= bound).all()), float((e / bound).max())
         assert bool((got[s, :, lk:] == 7).all())
     assert mea.device_error() == 0
+
+
+# ------------------------------------------------------------------------------ many short requests
+def test_many_short_requests_cost_what_they_do_in_batches():
+    """1024 requests of up to 600 keys in one call take no longer than in sixteen calls of 64: what a
+    CTA does besides its own request does not grow with the batch."""
+    n, hkv, d, bs, keep, part = 1024, 8, 64, 32, 128, 64
+    lens = torch.randint(16, 601, (n,), generator=torch.Generator().manual_seed(201))
+    nblk = [-(-int(x) // bs) for x in lens]
+    table = torch.zeros((n, max(nblk)), dtype=torch.int32)
+    at = 0
+    for b, m in enumerate(nblk):
+        table[b, :m] = torch.arange(at, at + m)
+        at += m
+    table = table.cuda()
+    kc = torch.zeros((at, bs, hkv, d), dtype=BF, device="cuda")
+    w = torch.rand((n, hkv, 600), device="cuda")
+    per = keep // bs
+    ot = torch.arange(n * per, dtype=torch.int32, device="cuda").view(n, per)
+    ko = torch.zeros((n * per, bs, hkv, d), dtype=BF, device="cuda")
+    bounds = torch.rand((at, hkv, 2, d), device="cuda").to(BF)
+    q = torch.rand((n, hkv, d), device="cuda").to(BF)
+
+    def step(a, b, cu):
+        mea.evict_paged(kc, kc, table[a:b], cu, 600, w[a:b], keep, 8, ot[a:b], out_k_cache=ko,
+                        out_v_cache=ko)
+        mea.select_blocks(q[a:b], bounds, table[a:b], cu, 600, bs, 4)
+
+    whole = cu_seqlens(lens.tolist()).cuda()
+    parts = [cu_seqlens(lens[a:a + part].tolist()).cuda() for a in range(0, n, part)]
+    calls = {"one": [(0, n, whole)],
+             "many": [(i * part, (i + 1) * part, cu) for i, cu in enumerate(parts)]}
+    times = {}
+    for name, args in list(calls.items()) * 2:  # (the second time counts)
+        start, end = torch.cuda.Event(True), torch.cuda.Event(True)
+        torch.cuda.synchronize()
+        start.record()
+        for _ in range(3):
+            for a in args:
+                step(*a)
+        end.record()
+        torch.cuda.synchronize()
+        times[name] = start.elapsed_time(end)
+    assert times["one"] <= 1.5 * times["many"], times
