@@ -321,3 +321,65 @@ def test_many_short_requests_cost_what_they_do_in_batches():
         torch.cuda.synchronize()
         times[name] = start.elapsed_time(end)
     assert times["one"] <= 1.5 * times["many"], times
+
+
+def test_as_many_blocks_as_can_be_chosen_from():
+    """50000 blocks of one request: the rank keys take all the shared memory there is."""
+    n_blocks, bs, d, hq = 50000, 16, 256, 2
+    length = n_blocks * bs - 3
+    table = torch.randperm(n_blocks, generator=torch.Generator().manual_seed(211)).view(1, -1)
+    bounds = randn((n_blocks, 1, 2, d), 212, FP, "cuda").sort(2).values
+    q = randn((1, hq, d), 213, FP, "cuda")
+    tab, cu = table.int().cuda(), cu_seqlens([length]).cuda()
+    got = mea.select_blocks(q, bounds, tab, cu, length, bs, 777).cpu()
+    x = q.double()[0]
+    up, down = x.clamp_min(0).sum(0), x.clamp_max(0).sum(0)
+    b = bounds[table[0].cuda(), 0].double()
+    score = (b[:, 1] @ up + b[:, 0] @ down).float()
+    score[0] = score[-1] = math.inf
+    order = torch.sort(score, descending=True, stable=True).indices[:777].sort().values
+    assert got[0, 0].tolist() == order.tolist()
+    with pytest.raises(mea.MeaError):
+        mea.select_blocks(q, bounds, torch.cat((tab, tab), 1), cu, length + 16, bs, 777)
+
+
+# ------------------------------------------------------------------------------------- any scale
+@pytest.mark.parametrize("scale", [-0.125, 0.0, 3.0])
+@pytest.mark.parametrize("alibi", [False, True])
+def test_scales_of_either_sign(scale, alibi):
+    """Scales that are not positive turn the order of the scores round, or leave the bias alone."""
+    lens, nq, hq, hkv, d, bs = [700, 129, 40], [9, 40, 1], 8, 2, 64, 16
+    c = ref.Cache(lens, hq, hkv, d, FP, bs, 221)
+    kc, vc, table, cu = c.gpu()
+    slopes = alibi_slope_values(hq) if alibi else None
+    gs = None if slopes is None else slopes.cuda()
+    q, tq = randn((3, hq, d), 222, FP), randn((sum(nq), hq, d), 223, FP)
+    every = torch.arange(44, dtype=torch.int32, device="cuda").expand(3, hkv, -1)
+    w = torch.zeros((3, hkv, 700), device="cuda")
+    o, m, z, want = ref.decode(c, q, scale, slopes)
+    for out, lse in (mea.decode_paged_selected(q.cuda(), kc, vc, table, cu, every,
+                                               alibi_slopes=gs, scale=scale),
+                     mea.decode_paged_weights(q.cuda(), kc, vc, table, cu, 700, w,
+                                              alibi_slopes=gs, scale=scale)[:2]):
+        ref.check_out(out.cpu(), lse.cpu(), o, m, z, FP)
+    for b, n in enumerate(lens):
+        x = torch.stack(want[b])
+        assert bool(((w.cpu()[b, :, :n].double() - x).abs() <= 2 * ref.F32 * x + 1e-30).all())
+    masks = [torch.ones(n, n, dtype=torch.bool).tril() for n in nq]
+    o, m, z = ref.tree(c, tq, nq, masks, scale, slopes)
+    out, lse = mea.decode_tree_paged(tq.cuda(), kc, vc, table, cu_seqlens(nq).cuda(), cu, 40, 700,
+                                     mea.tree_mask([list(range(-1, n - 1)) for n in nq]).cuda(),
+                                     alibi_slopes=gs, scale=scale)
+    ref.check_out(out.cpu(), lse.cpu(), o, m, z, FP)
+    k, v = torch.cat(c.k), torch.cat(c.v)
+    pq = randn((sum(lens), hq, d), 224, FP)
+    cp = cu_seqlens(lens).cuda()
+    _, lse = mea.attention_packed(pq.cuda(), k.cuda(), v.cuda(), cp, cp, 700, causal=True,
+                                  alibi_slopes=gs, scale=scale)
+    got = mea.attention_packed_weights(pq.cuda(), k.cuda(), lse, cp, cp, 700, 700, causal=True,
+                                       alibi_slopes=gs, scale=scale).cpu()
+    want = ref.prompt_weights(pq, k, lse.cpu(), lens, lens, scale, True, slopes, 0, 700)
+    for s, n in enumerate(lens):
+        assert bool(((got[s, :, :n].double() - want[s, :, :n]).abs() <=
+                     ref.F32 * want[s, :, :n] + 1e-30).all())
+    assert mea.device_error() == 0
