@@ -257,8 +257,10 @@ int mea_decode_paged(const void* q, const void* k_cache, const void* v_cache,
  * counts L_b, max_seqlen_k an upper bound on every L_b with max_blocks * block_size >=
  * max_seqlen_k, D a multiple of 8 from 8 to 256. A block id outside [0, num_blocks) reads as zeros,
  * and nothing is written for it (neither faults). Slots past a request's end may hold any bits.
- * Where max_seqlen_k is 0 (requests without keys) weights may be NULL. No atomics on results: every
- * result is deterministic. None of the calls allocates device memory or synchronises the host, and
+ * Where max_seqlen_k is 0 (requests without keys) weights may be NULL. Scores, sums, log-sum-exps and
+ * weights are fp32; the probabilities are rounded to dtype once before they multiply V, as in
+ * mea_forward, which moves an output by at most half a step of dtype of sum_j p_j |v_j| beside its own
+ * rounding. No atomics on results: every result is deterministic. None of the calls allocates device memory or synchronises the host, and
  * all can be captured into a CUDA graph; two calls that may run at the same time (two streams, two
  * graphs) need a workspace each.
  */
@@ -292,7 +294,8 @@ int mea_block_key_bounds(const void* k_cache, const int32_t* block_table,
  *   selected  DEVICE int32 [n_seqs, n_heads_kv, n_select]: block indices within the request (places
  *             in its block_table row), ascending, -1 after the last one when there are fewer.
  * ceil(max_seqlen_k / block_size) <= MEA_SELECT_MAX_BLOCKS; a request's blocks past that many are
- * not considered.
+ * not considered. The score is that of q . k under a positive scale: it knows no ALiBi term, so with
+ * slopes the blocks chosen are not those of the greatest biased scores (n_last keeps the nearest).
  */
 int mea_select_blocks(const void* q, const void* bounds, const int32_t* block_table,
                       const int32_t* cu_seqlens_k, int32_t* selected, int n_seqs, int num_blocks,

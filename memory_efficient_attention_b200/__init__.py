@@ -554,7 +554,8 @@ def block_key_bounds(k_cache: torch.Tensor, block_table: torch.Tensor,
     hold a key: ``bounds [num_blocks, Hkv, 2, D]`` in the cache's dtype, what
     :func:`select_blocks` reads. With ``first_key`` (int32 ``[n_seqs]``) only the blocks that hold a
     request's keys from ``first_key[b]`` on are done: after a decode step, its newest key's block.
-    Blocks in no request's table are left as they were (zeros when ``bounds`` is made here)."""
+    Blocks in no request's table are left as they were (zeros when ``bounds`` is made here). A block
+    that two requests share must be as full for both (a shared prefix of whole blocks is)."""
     idx, (nb, bs, hkv, d), code, table, cu = _check_paged(k_cache, None, block_table,
                                                           cu_seqlens_k)
     n, max_blocks = table.shape
@@ -579,7 +580,9 @@ def select_blocks(q: torch.Tensor, bounds: torch.Tensor, block_table: torch.Tens
     its last ``n_last``, and of the others those whose key ranges (:func:`block_key_bounds`) allow
     the greatest sum over the group's heads of ``q . k``. Returns int32
     ``[n_seqs, Hkv, n_select]``, block indices within the request in ascending order, -1 after the
-    last one when the request has fewer blocks. Equal scores: the lower index."""
+    last one when the request has fewer blocks. Equal scores: the lower index. The choice knows no
+    ALiBi term (:func:`decode_paged_selected` does): with slopes, ``n_last`` keeps the blocks that
+    the bias favours."""
     idx = _gpu_index(q)
     if q.dim() != 3 or bounds.dim() != 4 or bounds.size(2) != 2 or bounds.size(3) != q.size(2):
         raise MeaError(_lib.MEA_ERR_SHAPE, "q [n_seqs, Hq, D], bounds [num_blocks, Hkv, 2, D]")
@@ -754,7 +757,8 @@ def evict_paged(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch
     request still reads from). Returns ``(kept [n_seqs, Hkv, n_keep] int32, out_weights of the same
     shape, out_cu_seqlens_k [n_seqs + 1])``: the kept keys' indices (then -1) and weights (then 0)
     and the new prefix sums, in buffers other than the inputs' (lengths and weights are not updated
-    in place). Afterwards a slot holds another token's key for each head, so ALiBi no
+    in place). To go on adding up weights, copy ``out_weights`` to the front of zeroed rows as long
+    as the next keys need. Afterwards a slot holds another token's key for each head, so ALiBi no
     longer applies."""
     idx, (nb, bs, hkv, d), code, table, cu = _check_paged(k_cache, v_cache, block_table,
                                                           cu_seqlens_k)

@@ -395,8 +395,8 @@ int mea_evict_paged(const void* k_cache, const void* v_cache, const int32_t* blo
                     int num_out_blocks, int block_size, int max_blocks, int max_out_blocks,
                     int max_seqlen_k, int n_heads_kv, int head_dim, int n_keep, int n_recent,
                     int dtype, void* stream) {
-  if (!k_cache || !v_cache || !block_table || !cu_seqlens_k ||
-      (max_seqlen_k > 0 && !weights) || !out_k_cache || !out_v_cache || !out_table || !kept || !out_weights || !out_cu_seqlens_k)
+  if (!k_cache || !v_cache || !block_table || !cu_seqlens_k || (max_seqlen_k > 0 && !weights) ||
+      !out_k_cache || !out_v_cache || !out_table || !kept || !out_weights || !out_cu_seqlens_k)
     return MEA_ERR_NULL;
   if (int rc = check_cache(n_seqs, num_blocks, block_size, max_blocks, n_heads_kv, head_dim, dtype))
     return rc;

@@ -109,8 +109,8 @@ __device__ __forceinline__ int dec_nchunks(const int32_t* cu, int i, int chunk) 
 }
 
 // Keys per chunk. A paged decode's slots are sized by a bound on the requests' keys together (the
-// cache's slots, where the caller gives none), which requests that share blocks can exceed. Then the
-// chunks are as many times longer as the keys K exceed it, and the slots hold all of them:
+// cache's slots, where the caller gives none), which requests that share blocks can exceed. Then
+// the chunks are as many times longer as the keys K exceed it, and the slots hold all of them:
 //     sum_b ceil(L_b / chunk) <= K / chunk + n_seqs <= n_slots.
 // (The loads of K take at most 2 us of a call of 803: 64 requests of up to 32768 keys, 16 slots.)
 __device__ __forceinline__ int dec_chunk(const DecParams& p) {
@@ -592,6 +592,8 @@ __global__ void __launch_bounds__(160, 1)
           o[n][2] *= al_hi;
           o[n][3] *= al_hi;
         }
+        // (P rounded to V's 16-bit type, which the product wants of both: half a step of 16 bits of
+        // sum p |v| at most. The sums above and the weights' scores have the unrounded values.)
         uint32_t pa[4];
         pa[0] = dpack2<BF16>(pr[0][0], pr[0][1]);
         pa[1] = dpack2<BF16>(pr[0][2], pr[0][3]);
@@ -830,8 +832,8 @@ __global__ void __launch_bounds__(256) mea_selected_merge_kernel(const DecParams
 }
 
 // Merge and attention weights of a decode step, in one launch: CTA (0, g, b) merges the partial
-// outputs; thread t of CTA (1 + key range, KV head g, request b) takes four keys and adds exp2(score - lse) over the R heads of the group, in head order, to the key's
-// previous weight. The row's lse comes from its chunks' lse, as in the merge above.
+// outputs; thread t of CTA (1 + key range, KV head g, request b) takes four keys and adds
+// exp2(score - lse) over the R heads of the group, in head order, to the key's previous weight. The row's lse comes from its chunks' lse, as in the merge above.
 // Bound by memory: it reads the scores that the split kernel wrote (4 R bytes a key, part of
 // them still in L2) and reads and writes 4 bytes of weight a key.
 template <int D, bool BF16>

@@ -22,6 +22,11 @@
 // warpgroups take those rows and every second key tile each, so that one's softmax still runs
 // beside the other's products; the first then joins the two O, which lie in the same TMEM lanes.
 //
+// P is rounded to the inputs' 16-bit type before P V, as in the forward: the product takes both its
+// operands in one 16-bit type, and P in two 16-bit pieces would be half as many products again where
+// the products are the bound. It moves an output by at most half a step of 16 bits of sum p |v|; the
+// row sums and log-sum-exps come from the unrounded values, in fp32.
+//
 // Bound: with n_b R rows, a key costs 4 D bytes and 4 D n_b R flop; up to about 250 rows (bf16
 // peak over HBM rate) that is HBM-bound, beyond it the tensor cores are.
 #pragma once

@@ -28,9 +28,11 @@
 // slower).
 //
 // Bound by the exponentials: a score costs 2 D flop on the tensor cores and one exp2, and an SM does
-// 16 exp2 a clock: 1024 clocks for a 128 x 128 tile, whose product takes 512 at D = 128. (A quarter to
-// three eighths of them by a polynomial on the FMA pipes took fewer clocks and as much time or more:
-// the card is at its power limit here, and the longer instruction stream lowers the clock.)
+// 16 exp2 a clock: 1024 clocks for a 128 x 128 tile. Its product is not far behind: eight 128 x 128 x
+// 16 instructions at D = 128, 108 clocks each with both operands in shared memory (64 at the pipe's
+// peak), are 864. (A quarter to three eighths of the exponentials by a polynomial on the FMA pipes took
+// fewer clocks and as much time or more: the card is at its power limit here, and the longer
+// instruction stream lowers the clock.)
 #pragma once
 
 #include <cuda_bf16.h>

@@ -383,3 +383,55 @@ def test_scales_of_either_sign(scale, alibi):
         assert bool(((got[s, :, :n].double() - want[s, :, :n]).abs() <=
                      ref.F32 * want[s, :, :n] + 1e-30).all())
     assert mea.device_error() == 0
+
+
+# --------------------------------------------------------------------------------- a serving loop
+def test_tokens_after_an_eviction():
+    """Evict, append a token, decode with weights, and again: the kept weights go to the front of the
+    next step's rows, the new key adds its own, and the next eviction goes by both."""
+    total, hq, hkv, d, bs, keep, recent = [230, 60, 35], 8, 2, 64, 16, 40, 6
+    n, rounds = len(total), 3
+    c = ref.Cache([x + rounds for x in total], hq, hkv, d, BF, bs, 231)  # the later tokens' keys too
+    kc, vc, table, _ = c.gpu()
+    cu, max_k = cu_seqlens(total).cuda(), max(total)
+    w = torch.rand((n, hkv, max_k), generator=torch.Generator().manual_seed(232)).cuda()
+    old = w.cpu().double()
+    keys = [[list(range(x)) for _ in range(hkv)] for x in total]
+    per = -(-(keep + 1) // bs)
+    for step in range(rounds):
+        # (two sets of blocks, in turn: none is read and written by one eviction)
+        ko = torch.full((n * per, bs, hkv, d), math.nan, dtype=BF, device="cuda")
+        vo = torch.full_like(ko, math.nan)
+        ot = torch.randperm(n * per, generator=torch.Generator().manual_seed(step)).view(n, per)
+        ot = ot.int().cuda()
+        kept, ow, ocu = mea.evict_paged(kc, vc, table, cu, max_k, w, keep, recent, ot,
+                                        out_k_cache=ko, out_v_cache=vo)
+        lens = [min(x if step == 0 else len(keys[b][0]), keep) for b, x in enumerate(total)]
+        assert ocu.cpu().tolist() == cu_seqlens(lens).tolist()
+        was, now = old, torch.zeros((n, hkv, keep + 1)).double()
+        for b in range(n):
+            for g in range(hkv):
+                at = kept[b, g, :lens[b]].tolist()
+                m = max(0, len(keys[b][g]) - recent)
+                if len(keys[b][g]) > keep:
+                    order = sorted(range(m), key=lambda t: (-float(w[b, g, t]), t))
+                    assert at == sorted(order[:keep - recent]) + list(range(m, len(keys[b][g])))
+                now[b, g, :lens[b]] = was[b, g, at]
+                keys[b][g] = [keys[b][g][t] for t in at] + [total[b] + step]
+            ko[ot[b, lens[b] // bs], lens[b] % bs] = c.k[b][total[b] + step].cuda()
+            vo[ot[b, lens[b] // bs], lens[b] % bs] = c.v[b][total[b] + step].cuda()
+        cu = cu_seqlens([x + 1 for x in lens]).cuda()
+        kc, vc, table, max_k = ko, vo, ot, keep + 1
+        w = torch.zeros((n, hkv, max_k), device="cuda")
+        w[:, :, :keep] = ow
+        q = randn((n, hq, d), 240 + step, BF)
+        out, lse, _ = mea.decode_paged_weights(q.cuda(), kc, vc, table, cu, max_k, w,
+                                               prev_weights=w, scale=0.125)
+        o, m, z, p = ref.decode(c, q, 0.125, None, keys)
+        ref.check_out(out.cpu(), lse.cpu(), o, m, z, BF)
+        for b in range(n):
+            now[b, :, :lens[b] + 1] += torch.stack(p[b])
+        old = now
+        # fp32: the weights' own bound in every round so far, and the additions' rounding
+        assert bool(((w.cpu().double() - now).abs() <= (step + 2) * ref.F32 * now + 1e-30).all())
+    assert mea.device_error() == 0
